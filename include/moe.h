@@ -71,7 +71,9 @@ typedef enum {
   MOE_ERR_NONFINITE = 6    /* moe_validate_inputs found a NaN or an infinity */
 } moe_status;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1 } moe_dtype;
+/* MOE_F16 (IEEE half) is an element type of rows and activations where an entry point
+ * says so (a dtype argument of its own); dims->dtype is MOE_F32 or MOE_BF16. */
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_F16 = 2 } moe_dtype;
 
 /* What a null slot outputs (paper review section 3 compares null and copy
  * experts; the MoE++ page lists zero, copy and constant zero-compute experts).
@@ -94,7 +96,10 @@ typedef struct {
 } moe_dims;
 
 /* Which workspace size moe_workspace_bytes() returns. */
-enum { MOE_WS_LAYER = 0, MOE_WS_ROUTE = 1, MOE_WS_PERMUTE = 2, MOE_WS_AUX = 3, MOE_WS_BACKWARD = 4 };
+enum {
+  MOE_WS_LAYER = 0, MOE_WS_ROUTE = 1, MOE_WS_PERMUTE = 2, MOE_WS_AUX = 3, MOE_WS_BACKWARD = 4,
+  MOE_WS_COMBINE_BACKWARD = 5
+};
 
 typedef void* moe_stream; /* hipStream_t */
 
@@ -256,6 +261,124 @@ moe_status moe_combine(const moe_dims* dims, const void* y_perm, const int32_t* 
 moe_status moe_aux_stats(const moe_dims* dims, const float* logits, const int32_t* topk_idx,
                          float* f, float* P, int32_t* counts, float* scalars, void* ws,
                          size_t ws_bytes, moe_stream stream);
+
+/*
+ * moe_combine_rows -- moe_combine for expert rows of any storage type (experts outside
+ * this library answer in the type they compute in). Same formula, slot rules and
+ * arithmetic as moe_combine (paper review section 3, core formula): summed in slot
+ * order in float32, one rounding, no atomics.
+ * rows_dtype: MOE_F32, MOE_BF16 or MOE_F16, the type of y_perm and y_shared; null_src
+ * and y are dims->dtype.
+ * d_model at most 2^30 here and in the two gradients below (else MOE_ERR_UNSUPPORTED).
+ * Output buffers must not overlap inputs or each other unless stated.
+ */
+moe_status moe_combine_rows(const moe_dims* dims, int32_t rows_dtype, const void* y_perm,
+                            const int32_t* slot_pos, const float* topk_w, const void* y_shared,
+                            const void* null_src, void* y, moe_stream stream);
+
+/*
+ * moe_combine_backward -- gradients of moe_combine and moe_combine_rows (paper review
+ * section 3, core formula) for the upstream gradient dy [T][d] dims->dtype. For every
+ * real slot (t, k) at p = slot_pos[t][k]:
+ *   dy_perm[p]  = topk_w[t][k] dy_t    [T*min(K,N)][d] rows_dtype (gradient of y_perm)
+ *   w_perm[p]   = topk_w[t][k]         [T*min(K,N)] float32
+ *   row_slot[p] = t K + k              [T*min(K,N)] int32
+ *   dtopk_w[t][k] = <dy_t, y_perm[p]>  [T][K] float32
+ * and for the null slots (slot_pos = -1): dtopk_w = 0 with MOE_NULL_ZERO, <dy_t, x_t>
+ * with MOE_NULL_COPY and <dy_t, v> with MOE_NULL_CONSTANT (null_src as in moe_combine,
+ * required for those two). Other slots outside [0, T*min(K,N)) get dtopk_w = 0.
+ *   dnull: MOE_NULL_COPY [T][d] float32, (sum of the token's null weights) dy_t, 0 for a
+ *   token without null slots; MOE_NULL_CONSTANT [d] float32, the sum of those over all
+ *   tokens (float32 sums of 64 tokens, joined in float64 in a fixed order);
+ *   ignored with MOE_NULL_ZERO.
+ * The shared expert's gradient is dy itself. Every output may be NULL (not computed).
+ * y_perm may be NULL when the expert outputs were not kept: dtopk_w of the real slots
+ * is then left unwritten (moe_swiglu_backward8 can supply it through row_slot). Rows of
+ * the outputs in expert order that no slot names are left unwritten. Positions are as
+ * moe_permute writes them, no two slots at the same one (of two that share one, either's
+ * product is stored). Deterministic, no atomics.
+ * ws: MOE_WS_COMBINE_BACKWARD bytes (only MOE_NULL_CONSTANT with dnull needs any).
+ */
+moe_status moe_combine_backward(const moe_dims* dims, int32_t rows_dtype, const void* dy,
+                                const void* y_perm, const int32_t* slot_pos, const float* topk_w,
+                                const void* null_src, void* dy_perm, float* w_perm,
+                                int32_t* row_slot, float* dtopk_w, float* dnull, void* ws,
+                                size_t ws_bytes, moe_stream stream);
+
+/*
+ * moe_permute_backward -- gradient of moe_permute's gather x_perm[p] = x[perm_token[p]]
+ * (paper review section 3 "implementation"):
+ *   dx_t = dx_add_t + sum over the token's real slots of dx_perm[slot_pos[t][k]]
+ * summed in slot order in float32 from dx_add, rounded once. Slots outside
+ * [0, T*min(K,N)) add nothing; a token without real slots gets dx_add_t (or 0).
+ * dx_perm: [T*min(K,N)][d] rows_dtype; dx_add: [T][d] float32 or NULL (the shared
+ * expert's, the router's or a copied token's gradient); dx: [T][d] dx_dtype. Types
+ * MOE_F32, MOE_BF16 or MOE_F16. dx may be dx_add itself (float32).
+ */
+moe_status moe_permute_backward(const moe_dims* dims, int32_t rows_dtype, const void* dx_perm,
+                                const int32_t* slot_pos, const float* dx_add, int32_t dx_dtype,
+                                void* dx, moe_stream stream);
+
+/*
+ * 8-bit activation checkpoints (the paper review, section 4 "training configuration",
+ * trains the layer; the pages do not fix what a step keeps). A tensor [rows][cols] is
+ * held as codes int8 [rows][cols] and one scale byte per block of 32 columns,
+ * scales uint8 [rows][ceil(cols / 32)] (the last block of a row may be shorter). With
+ * amax the largest magnitude in the block:
+ *   e = max(floor(log2 amax) - 6, -126);  scale byte = e + 127
+ *   code q = clamp(rint(v 2^-e), -127, 127) (ties to even), standing for q 2^e
+ * so |v - q 2^e| <= 2^(e-1), or 2^e where |v| > 127.5 2^e. Codes and values are exact
+ * functions of the input. A block with a NaN or an infinity has scale byte 255 and
+ * codes 0 and stands for NaN. The sign of a zero is lost.
+ * Conventions of these entry points (no dims):
+ *   - dtype arguments: MOE_F32, MOE_BF16 or MOE_F16. cols and d_ff are multiples of 8;
+ *     rows >= 0, rows = 0 is a no-op; rows * cols < 2^40.
+ *   - ld arguments: elements from one row to the next, a multiple of 8, at least cols
+ *     (so gate and up may be the halves of one [rows][2 d_ff] matrix). Other tensors
+ *     are dense.
+ *   - n_rows: optional DEVICE int32; only rows below clamp(n_rows[0], 0, rows) are read
+ *     and written (offsets + N of moe_permute gives the real slots; it needs 4-byte
+ *     alignment only). No workspace.
+ *   - output buffers must not overlap inputs or each other.
+ */
+moe_status moe_act8_pack(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ldx,
+                         const int32_t* n_rows, int8_t* codes, uint8_t* scales, moe_stream stream);
+/* The values a checkpoint stands for, rounded to dtype (exact in MOE_F32 and MOE_BF16, and
+ * in MOE_F16 for the checkpoint of a MOE_F16 tensor). */
+moe_status moe_act8_unpack(int64_t rows, int32_t cols, int32_t dtype, const int8_t* codes,
+                           const uint8_t* scales, const int32_t* n_rows, void* out, int64_t ldo,
+                           moe_stream stream);
+
+/*
+ * moe_swiglu_keep8 -- the expert activation h = silu(g) u (quant67 primer section 2, in
+ * SwiGLU form) and the 8-bit checkpoints of g and u, in one pass. g, u: [rows][ld]
+ * dtype; h: [rows][d_ff] dtype, from the unrounded-to-8-bits g and u (float32 inside,
+ * one rounding); codes and scales as above, [rows][d_ff] each.
+ */
+moe_status moe_swiglu_keep8(int64_t rows, int32_t d_ff, int32_t dtype, const void* g, const void* u,
+                            int64_t ld, const int32_t* n_rows, void* h, int8_t* codes_g,
+                            uint8_t* scales_g, int8_t* codes_u, uint8_t* scales_u, moe_stream stream);
+
+/*
+ * moe_swiglu_backward8 -- the SwiGLU backward from those checkpoints. With z and u the
+ * values the checkpoints stand for, s = 1 / (1 + exp(-z)), w_p = w_rows[p] (1 if NULL):
+ *   dg_p = w_p dh_p u s (1 + z (1 - s));  du_p = w_p dh_p z s;  h_p = z s u
+ *   dw[row_slot[p]] (dw[p] if row_slot is NULL) = sum over columns of dh_p h_p
+ * dh: [rows][d_ff] dh_dtype; dg, du: [rows][ld] out_dtype; h: [rows][d_ff] out_dtype or
+ * NULL (the weight gradient's operand, so h need not be kept). w_rows: [rows] float32 or
+ * NULL, dw: float32 or NULL, row_slot: [rows] int32 or NULL, n_slots the length of dw
+ * (entries of row_slot outside [0, n_slots) are skipped; no two rows at the same one).
+ * With dh = dy W_down^T of the unweighted output gradient and w_rows, row_slot from
+ * moe_combine_backward, dw is the routing weights' gradient, expert outputs not kept.
+ * Sums in float32 in a fixed order; a row's sum runs over the checkpoint's h before its
+ * rounding to out_dtype.
+ */
+moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_g,
+                                const uint8_t* scales_g, const int8_t* codes_u,
+                                const uint8_t* scales_u, const int32_t* n_rows, int32_t dh_dtype,
+                                const void* dh, const float* w_rows, const int32_t* row_slot,
+                                int64_t n_slots, int32_t out_dtype, void* dg, void* du, int64_t ld,
+                                void* h, float* dw, moe_stream stream);
 
 /* Device pointers of the layer's inputs. */
 typedef struct {

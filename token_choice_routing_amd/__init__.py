@@ -21,10 +21,11 @@ LIB_PATH = os.path.join(HERE, "libmoe_mi355x.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moe.h")
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP, MOE_ERR_NONFINITE = range(7)
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_NULL_ZERO, MOE_NULL_COPY, MOE_NULL_CONSTANT = 0, 1, 2
 NULL_KINDS = {"zero": MOE_NULL_ZERO, "copy": MOE_NULL_COPY, "constant": MOE_NULL_CONSTANT}
-MOE_WS_LAYER, MOE_WS_ROUTE, MOE_WS_PERMUTE, MOE_WS_AUX, MOE_WS_BACKWARD = range(5)
+(MOE_WS_LAYER, MOE_WS_ROUTE, MOE_WS_PERMUTE, MOE_WS_AUX, MOE_WS_BACKWARD,
+ MOE_WS_COMBINE_BACKWARD) = range(6)
 MOE_GEMM_GATE_UP, MOE_GEMM_DOWN = 0, 1
 
 
@@ -68,7 +69,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run `python -m token_choice_routing_amd.build`")
     lib = ctypes.CDLL(path)
-    D = ctypes.POINTER(Dims)
+    D, I, L = ctypes.POINTER(Dims), ctypes.c_int32, ctypes.c_int64
     sig = {
         "moe_route": [D, _P, _P, ctypes.c_float, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_permute": [D, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
@@ -78,6 +79,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_expert_gate_up": [D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P],
         "moe_grouped_gemm": [D, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
                              ctypes.c_int64, _P, _P, _P, _P, _P, _P],
+        "moe_combine_rows": [D, I, _P, _P, _P, _P, _P, _P, _P],
+        "moe_combine_backward": [D, I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
+        "moe_permute_backward": [D, I, _P, _P, _P, I, _P, _P],
+        "moe_act8_pack": [L, I, I, _P, L, _P, _P, _P, _P],
+        "moe_act8_unpack": [L, I, I, _P, _P, _P, _P, L, _P],
+        "moe_swiglu_keep8": [L, I, I, _P, _P, L, _P, _P, _P, _P, _P, _P, _P],
+        "moe_swiglu_backward8": [L, I, _P, _P, _P, _P, _P, I, _P, _P, _P, L, I, _P, _P, L, _P, _P, _P],
         "moe_aux_stats": [D, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_layer_forward": [D, ctypes.POINTER(LayerParams), _P, ctypes.POINTER(AuxOut), _P,
                               ctypes.c_size_t, _P],
@@ -136,6 +144,58 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+_ROW_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
+_DTYPES = {v: k for k, v in _ROW_TYPES.items()}
+_EMPTY = 256  # address of a tensor without elements (torch has none): nothing of it is accessed
+
+
+def _arg(name, t, dtype=None, shape=None, optional=False):
+    """Device address of a tensor argument whose type and shape the call fixes. The
+    library sees addresses only, so a tensor of another type, a smaller one or one on
+    another device than the current one is refused here (an int is taken as an address
+    as is)."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if isinstance(t, int):
+        return t
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current device, got one on {t.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr() if t.numel() else _EMPTY
+
+
+def _matrix(name, t, dtype=None, shape=None):
+    """(device address, elements from row to row) of a [rows][cols] tensor whose rows may
+    be spaced (a column range of a wider matrix) but are dense inside."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: expected a tensor on the current device, got one on {t.device}")
+    if t.dim() != 2 or t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name}: expected a matrix of {dtype or 'float32, bfloat16 or float16'}, got "
+                         f"{tuple(t.shape)} of {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    rows, cols = t.shape
+    ld = t.stride(0) if rows > 1 else cols
+    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+        raise ValueError(f"{name}: expected rows that are dense and do not overlap, got strides {t.stride()}")
+    return (t.data_ptr() if t.numel() else _EMPTY), ld
+
+
+def _row_dtype(name, code):
+    if code not in _DTYPES:
+        raise ValueError(f"{name}: expected MOE_F32, MOE_BF16 or MOE_F16, got {code}")
+    return _DTYPES[code]
 
 
 def _check(status, where):
@@ -224,6 +284,130 @@ def moe_combine(dims, y_perm, slot_pos, topk_w, y_shared, y, stream=None, null_s
                                        _ptr(topk_w), _ptr(y_shared), _ptr(null_src), _ptr(y),
                                        _stream(stream)),
            "moe_combine")
+
+
+def _slot_shapes(dims):
+    """(dims dtype, [T][d], slot shape [T][K], rows in expert order) of a dispatch call."""
+    T, K, d = dims.T, dims.top_k, dims.d_model
+    return _DTYPES.get(dims.dtype), (T, d), (T, K), T * min(K, dims.n_experts)
+
+
+def moe_combine_rows(dims, rows_dtype, y_perm, slot_pos, topk_w, y_shared, y, null_src=None, stream=None):
+    """moe_combine with y_perm and y_shared of type rows_dtype (MOE_F32, MOE_BF16 or
+    MOE_F16). null_src: the rows a null slot adds (x for copy experts, v for constant)."""
+    dt, token, slots, cap = _slot_shapes(dims)
+    rt = _row_dtype("rows_dtype", rows_dtype)
+    nul = (dims.d_model,) if dims.null_kind == MOE_NULL_CONSTANT else token
+    _check(load_library().moe_combine_rows(
+        ctypes.byref(dims), rows_dtype, _arg("y_perm", y_perm, rt, (cap, dims.d_model)),
+        _arg("slot_pos", slot_pos, torch.int32, slots), _arg("topk_w", topk_w, torch.float32, slots),
+        _arg("y_shared", y_shared, rt, token, True),
+        _arg("null_src", null_src, dt, nul, True) if dims.null_kind != MOE_NULL_ZERO else None,
+        _arg("y", y, dt, token), _stream(stream)), "moe_combine_rows")
+
+
+def moe_combine_backward(dims, rows_dtype, dy, y_perm, slot_pos, topk_w, dy_perm=None, w_perm=None, row_slot=None,
+                         dtopk_w=None, null_src=None, dnull=None, ws=None, stream=None):
+    """Gradients of moe_combine / moe_combine_rows: dy_perm (rows_dtype), dtopk_w and the
+    null source's dnull; w_perm and row_slot hold each expert row's weight and flat slot
+    index. Every output is optional. ws: MOE_WS_COMBINE_BACKWARD bytes (constant nulls
+    with dnull)."""
+    dt, token, slots, cap = _slot_shapes(dims)
+    rt, f32 = _row_dtype("rows_dtype", rows_dtype), torch.float32
+    nul = (dims.d_model,) if dims.null_kind == MOE_NULL_CONSTANT else token
+    null = dims.null_kind != MOE_NULL_ZERO
+    wp, wb = _ws(ws)
+    _check(load_library().moe_combine_backward(
+        ctypes.byref(dims), rows_dtype, _arg("dy", dy, dt, token),
+        _arg("y_perm", y_perm, rt, (cap, dims.d_model), True), _arg("slot_pos", slot_pos, torch.int32, slots),
+        _arg("topk_w", topk_w, f32, slots), _arg("null_src", null_src, dt, nul, True) if null else None,
+        _arg("dy_perm", dy_perm, rt, (cap, dims.d_model), True), _arg("w_perm", w_perm, f32, (cap,), True),
+        _arg("row_slot", row_slot, torch.int32, (cap,), True), _arg("dtopk_w", dtopk_w, f32, slots, True),
+        _arg("dnull", dnull, f32, nul, True) if null else None, wp, wb, _stream(stream)), "moe_combine_backward")
+
+
+def moe_permute_backward(dims, rows_dtype, dx_perm, slot_pos, dx_add, dx_dtype, dx, stream=None):
+    """Gradient of moe_permute's gather: dx = dx_add (float32, optional) + the sum of each
+    token's real rows of dx_perm (rows_dtype), in dx_dtype; dx may be dx_add itself."""
+    _, token, slots, cap = _slot_shapes(dims)
+    rt, dt = _row_dtype("rows_dtype", rows_dtype), _row_dtype("dx_dtype", dx_dtype)
+    _check(load_library().moe_permute_backward(
+        ctypes.byref(dims), rows_dtype, _arg("dx_perm", dx_perm, rt, (cap, dims.d_model)),
+        _arg("slot_pos", slot_pos, torch.int32, slots), _arg("dx_add", dx_add, torch.float32, token, True),
+        dx_dtype, _arg("dx", dx, dt, token), _stream(stream)), "moe_permute_backward")
+
+
+ACT8_BLOCK = 32  # columns that share a scale byte
+
+
+def act8_scales_shape(rows, cols):
+    """Shape of the uint8 scales of a [rows][cols] checkpoint (its codes are int8 [rows][cols])."""
+    return rows, -(-cols // ACT8_BLOCK)
+
+
+def _kept(name, rows, cols, codes, scales):
+    return (_arg(f"{name}codes", codes, torch.int8, (rows, cols)),
+            _arg(f"{name}scales", scales, torch.uint8, act8_scales_shape(rows, cols)))
+
+
+def _live(n_rows):
+    return _arg("n_rows", n_rows, torch.int32, (1,), True)
+
+
+def moe_act8_pack(x, codes, scales, n_rows=None, stream=None):
+    """8-bit checkpoint of x [rows][cols] (float32, bfloat16 or float16; rows may be
+    spaced): codes int8 [rows][cols], scales uint8 [rows][ceil(cols / 32)]. n_rows: device
+    int32 [1], the rows in use (all if None); the others are left as they were."""
+    px, ld = _matrix("x", x)
+    rows, cols = x.shape
+    _check(load_library().moe_act8_pack(rows, cols, _ROW_TYPES[x.dtype], px, ld, _live(n_rows),
+                                        *_kept("", rows, cols, codes, scales), _stream(stream)), "moe_act8_pack")
+
+
+def moe_act8_unpack(codes, scales, out, n_rows=None, stream=None):
+    """The values a checkpoint stands for, into out [rows][cols] (rows may be spaced)."""
+    po, ld = _matrix("out", out)
+    rows, cols = out.shape
+    _check(load_library().moe_act8_unpack(rows, cols, _ROW_TYPES[out.dtype], *_kept("", rows, cols, codes, scales),
+                                          _live(n_rows), po, ld, _stream(stream)), "moe_act8_unpack")
+
+
+def moe_swiglu_keep8(g, u, h, g_codes, g_scales, u_codes, u_scales, n_rows=None, stream=None):
+    """h = silu(g) u and the 8-bit checkpoints of g and u. g, u: [rows][d_ff] of one type,
+    with the same spacing of rows; h: dense, the same type."""
+    pg, ld = _matrix("g", g)
+    pu, ldu = _matrix("u", u, g.dtype, g.shape)
+    rows, F = g.shape
+    if ld != ldu:
+        raise ValueError(f"g and u: expected the same spacing of rows, got {ld} and {ldu}")
+    _check(load_library().moe_swiglu_keep8(
+        rows, F, _ROW_TYPES[g.dtype], pg, pu, ld, _live(n_rows), _arg("h", h, g.dtype, g.shape),
+        *_kept("g_", rows, F, g_codes, g_scales), *_kept("u_", rows, F, u_codes, u_scales), _stream(stream)),
+        "moe_swiglu_keep8")
+
+
+def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=None, w_rows=None, dw=None,
+                         row_slot=None, n_rows=None, stream=None):
+    """The SwiGLU backward from the checkpoints of g and u: dg, du (one type, rows may be
+    spaced alike), optionally h (the same type, dense) and dw = <dh, h> per row (at
+    dw[row_slot[p]] when row_slot is given). w_rows scales dh per row in dg and du."""
+    pg, ld = _matrix("dg", dg)
+    pu, ldu = _matrix("du", du, dg.dtype, dg.shape)
+    rows, F = dg.shape
+    if ld != ldu:
+        raise ValueError(f"dg and du: expected the same spacing of rows, got {ld} and {ldu}")
+    pd, ldd = _matrix("dh", dh, None, dg.shape)
+    if ldd != F:
+        raise ValueError("dh: expected a contiguous tensor")
+    f32 = torch.float32
+    if dw is not None and row_slot is None and dw.numel() != rows:
+        raise ValueError(f"dw: expected {rows} elements, got {dw.numel()}")
+    _check(load_library().moe_swiglu_backward8(
+        rows, F, *_kept("g_", rows, F, g_codes, g_scales), *_kept("u_", rows, F, u_codes, u_scales), _live(n_rows),
+        _ROW_TYPES[dh.dtype], pd, _arg("w_rows", w_rows, f32, (rows,), True),
+        _arg("row_slot", row_slot, torch.int32, (rows,), True), 0 if dw is None else dw.numel(),
+        _ROW_TYPES[dg.dtype], pg, pu, ld, _arg("h", h, dg.dtype, dg.shape, True), _arg("dw", dw, f32, None, True),
+        _stream(stream)), "moe_swiglu_backward8")
 
 
 def moe_aux_stats(dims, logits, topk_idx, f, P, counts, scalars, ws, stream=None):

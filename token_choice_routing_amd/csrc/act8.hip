@@ -1,0 +1,313 @@
+// Activation checkpoints in 8 bits: pack, unpack, the SwiGLU that keeps its gate and up
+// projections so, and the SwiGLU backward that reads them.
+//
+// A training step keeps the expert pre-activations g and u from the forward to the
+// backward ([Review] section 4 trains the layer; which state a step keeps is not fixed
+// by the pages). Rows are cut into blocks of 32 columns (the last one of a row may be
+// shorter). With amax the largest magnitude in a block,
+//   e = max(floor(log2 amax) - 6, -126),  q = clamp(rint(v 2^-e), -127, 127),
+// the code q (int8) stands for q 2^e, and the block's scale byte is e + 127: float32
+// exponent bits, so the scale and every product with it are exact and the codes do not
+// depend on how they are computed. |v - q 2^e| <= 2^(e-1), or 2^e where |v| > 127.5 2^e
+// is clamped; against the block's largest value that is at most 2^-7 (2^-6 clamped).
+// int8 steps are uniform, so a block's error goes by its largest value; an 8-bit float
+// (4 significant bits) would be off by up to 2^-4 of that value itself. A block that
+// holds a NaN or an infinity has scale byte 255 and codes 0 and stands for NaN.
+//
+// Every kernel moves 8 columns per lane and step: a block is four adjacent lanes, whose
+// maxima meet in two quad permutations. All are bound by HBM.
+#include <algorithm>
+#include <type_traits>
+
+#include "common.hpp"
+#include "kernels.hpp"
+#include "rows.hpp"
+
+namespace moe {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kCols = 8;    // columns per lane and step
+constexpr int kQuad = 4;    // lanes per block of 32 columns
+
+__device__ __forceinline__ int64_t live_rows(const int32_t* n_rows, int64_t rows) {
+  return n_rows ? min<int64_t>(max<int64_t>(n_rows[0], 0), rows) : rows;
+}
+
+// Largest of a value over the four lanes of a quad.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
+  return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+}
+
+// The quad's scale byte for eight values per lane (lanes past the row hold zeros). As
+// integers, magnitudes order like the floats, with NaN above infinity.
+__device__ __forceinline__ uint32_t block_scale(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
+  m = quad_max(m) >> 23;  // biased exponent of amax: floor(log2 amax) + 127 (0: below 2^-126)
+  return m == 255 ? 255 : (uint32_t)max((int)m - 6, 1);
+}
+
+// Eight codes: v 2^-e + 1.5 2^23 rounds to an integer (nearest even) in the low bits.
+__device__ __forceinline__ u32x2_t encode(const float* v, uint32_t scale) {
+  if (scale == 255) return u32x2_t{0, 0};
+  const float inv = __uint_as_float((254 - scale) << 23);  // 2^-e
+  constexpr float kMagic = 12582912.0f;
+  uint32_t q[kCols];
+#pragma unroll
+  for (int j = 0; j < kCols; ++j)
+    q[j] = __float_as_uint(fminf(fmaxf(fmaf(v[j], inv, kMagic), kMagic - 127.0f), kMagic + 127.0f)) & 0xff;
+  return u32x2_t{q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24), q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24)};
+}
+
+// Eight values q 2^e, exact (0 times the NaN block's infinite scale is NaN).
+__device__ __forceinline__ void decode(u32x2_t c, uint32_t scale, float* v) {
+  const float s = __uint_as_float(scale << 23);
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) v[j] = (float)(int8_t)(c[j >> 2] >> (8 * (j & 3))) * s;
+}
+
+// Where thread i of a launch works: rows of cpr8 padded steps (a multiple of four, so a
+// quad stays in its block), the division by cpr8 as a multiplication (exact for i < 2^32).
+struct RowMap {
+  uint32_t cpr8;   // steps per row, rounded up to a multiple of 4
+  uint32_t steps;  // steps per row
+  uint64_t magic;  // floor(2^64 / cpr8) + 1
+};
+__device__ __forceinline__ void locate(const RowMap& m, uint32_t i, uint32_t& row, uint32_t& step) {
+  const uint64_t lo = (uint64_t)i * (uint32_t)m.magic, hi = (uint64_t)i * (uint32_t)(m.magic >> 32);
+  row = (uint32_t)((hi + (lo >> 32)) >> 32);
+  step = i - row * m.cpr8;
+}
+
+// One step of 8 columns after another over the live rows, f(row, column, on); a lane off
+// the row's end still takes part in its quad. A workgroup takes kThreads consecutive
+// steps at a time from a 64-bit base, so rows are counted from the base's row.
+template <typename F>
+__device__ __forceinline__ void for_steps(const RowMap& m, int64_t rows, F&& f) {
+  const int64_t total = rows * m.cpr8;
+  for (int64_t base = (int64_t)blockIdx.x * kThreads; base < total; base += (int64_t)gridDim.x * kThreads) {
+    const int64_t row0 = base / m.cpr8;
+    uint32_t row, step;
+    locate(m, (uint32_t)(base - row0 * m.cpr8) + threadIdx.x, row, step);
+    if (row0 + row < rows) f(row0 + row, (int64_t)step * kCols, step < m.steps);
+  }
+}
+
+template <typename XT>
+__global__ void __launch_bounds__(kThreads)
+act8_pack_kernel(const XT* __restrict__ x, int64_t ldx, const int32_t* __restrict__ n_rows, int64_t rows, int cols,
+                 RowMap m, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t nb = (cols + 31) / 32;
+  for_steps(m, live_rows(n_rows, rows), [&](int64_t row, int64_t col, bool on) {
+    float v[kCols] = {};
+    if (on) load_row<kCols>(x + row * ldx + col, v);
+    const uint32_t s = block_scale(v);
+    if (on) *reinterpret_cast<u32x2_t*>(codes + row * cols + col) = encode(v, s);
+    if (on && (col & 31) == 0) scales[row * nb + col / 32] = (uint8_t)s;
+  });
+}
+
+template <typename XT>
+__global__ void __launch_bounds__(kThreads)
+act8_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
+                   const int32_t* __restrict__ n_rows, int64_t rows, int cols, RowMap m, XT* __restrict__ out,
+                   int64_t ldo) {
+  const int64_t nb = (cols + 31) / 32;
+  for_steps(m, live_rows(n_rows, rows), [&](int64_t row, int64_t col, bool on) {
+    if (!on) return;
+    float v[kCols];
+    decode(*reinterpret_cast<const u32x2_t*>(codes + row * cols + col), scales[row * nb + col / 32], v);
+    store_row<kCols>(out + row * ldo + col, v);
+  });
+}
+
+// 1 / (1 + e^-z). For 16-bit results the hardware's exponential and reciprocal (a few
+// 2^-22 relative, far below their half steps of 2^-9 and 2^-12); float32 results take
+// the full-precision functions.
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float z) {
+  if constexpr (FAST) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
+  return 1.0f / (1.0f + expf(-z));
+}
+
+template <typename XT>
+__global__ void __launch_bounds__(kThreads)
+swiglu_keep8_kernel(const XT* __restrict__ g, const XT* __restrict__ u, int64_t ld, const int32_t* __restrict__ n_rows,
+                    int64_t rows, int F, RowMap m, XT* __restrict__ h, uint8_t* __restrict__ cg,
+                    uint8_t* __restrict__ sg, uint8_t* __restrict__ cu, uint8_t* __restrict__ su) {
+  const int64_t nb = (F + 31) / 32;
+  for_steps(m, live_rows(n_rows, rows), [&](int64_t row, int64_t col, bool on) {
+    float z[kCols] = {}, v[kCols] = {};
+    if (on) {
+      load_row<kCols>(g + row * ld + col, z);
+      load_row<kCols>(u + row * ld + col, v);
+    }
+    const uint32_t bz = block_scale(z), bv = block_scale(v);
+    if (!on) return;
+    *reinterpret_cast<u32x2_t*>(cg + row * F + col) = encode(z, bz);
+    *reinterpret_cast<u32x2_t*>(cu + row * F + col) = encode(v, bv);
+    if ((col & 31) == 0) {
+      sg[row * nb + col / 32] = (uint8_t)bz;
+      su[row * nb + col / 32] = (uint8_t)bv;
+    }
+    float o[kCols];
+#pragma unroll
+    for (int j = 0; j < kCols; ++j) o[j] = z[j] * sigmoid<sizeof(XT) == 2>(z[j]) * v[j];
+    store_row<kCols>(h + row * F + col, o);
+  });
+}
+
+// Eight columns of the SwiGLU backward. Returns the sum of dh h over them.
+template <bool FAST>
+__device__ __forceinline__ float swiglu_grad(const float* z, const float* u, const float* dh, float w, float* dg,
+                                             float* du, float* h) {
+  float dot = 0.0f;
+#pragma unroll
+  for (int j = 0; j < kCols; ++j) {
+    const float s = sigmoid<FAST>(z[j]), a = z[j] * s, d = w * dh[j];
+    h[j] = a * u[j];
+    dot = fmaf(dh[j], h[j], dot);
+    dg[j] = d * u[j] * (s * (1.0f + z[j] * (1.0f - s)));
+    du[j] = d * a;
+  }
+  return dot;
+}
+
+struct Bwd8 {
+  const uint8_t *cg, *sg, *cu, *su;
+  const int32_t* n_rows;
+  const float* w_rows;
+  const int32_t* row_slot;
+  float* dw;
+  int64_t n_slots, rows, ld;
+  int F;
+};
+
+template <typename DT, typename OT>
+__device__ __forceinline__ float swiglu_bwd8_step(const Bwd8& a, const DT* dh, OT* dg, OT* du, OT* h, int64_t nb,
+                                                  int64_t row, int64_t col, float w) {
+  float z[kCols], u[kCols], d[kCols], og[kCols], ou[kCols], oh[kCols];
+  const int64_t at = row * a.F + col, b = row * nb + col / 32;
+  const u32x2_t qz = *reinterpret_cast<const u32x2_t*>(a.cg + at), qu = *reinterpret_cast<const u32x2_t*>(a.cu + at);
+  const uint32_t bz = a.sg[b], bu = a.su[b];
+  load_row<kCols>(dh + at, d);
+  decode(qz, bz, z);
+  decode(qu, bu, u);
+  const float dot = swiglu_grad<sizeof(OT) == 2>(z, u, d, w, og, ou, oh);
+  store_row<kCols>(dg + row * a.ld + col, og);
+  store_row<kCols>(du + row * a.ld + col, ou);
+  if (h) store_row<kCols>(h + at, oh);
+  return dot;
+}
+
+// Rows without weight gradients: steps of 8 columns, any row to any lane.
+template <typename DT, typename OT>
+__global__ void __launch_bounds__(kThreads)
+swiglu_bwd8_kernel(Bwd8 a, RowMap m, const DT* __restrict__ dh, OT* __restrict__ dg, OT* __restrict__ du,
+                   OT* __restrict__ h) {
+  const int64_t nb = (a.F + 31) / 32;
+  for_steps(m, live_rows(a.n_rows, a.rows), [&](int64_t row, int64_t col, bool on) {
+    if (on) swiglu_bwd8_step(a, dh, dg, du, h, nb, row, col, a.w_rows ? a.w_rows[row] : 1.0f);
+  });
+}
+
+// Rows with weight gradients dw = <dh, h>: one wavefront per row, lane sums added in a
+// fixed order.
+template <typename DT, typename OT>
+__global__ void __launch_bounds__(kThreads)
+swiglu_bwd8_row_kernel(Bwd8 a, const DT* __restrict__ dh, OT* __restrict__ dg, OT* __restrict__ du,
+                       OT* __restrict__ h) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t n = live_rows(a.n_rows, a.rows), nb = (a.F + 31) / 32;
+  const int64_t nwaves = (int64_t)gridDim.x * (kThreads / kWave);
+  for (int64_t row = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; row < n; row += nwaves) {
+    const float w = a.w_rows ? a.w_rows[row] : 1.0f;
+    float dot = 0.0f;
+    for (int64_t col = lane * kCols; col < a.F; col += kWave * kCols)
+      dot += swiglu_bwd8_step(a, dh, dg, du, h, nb, row, col, w);
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
+    if (lane == 0) {
+      const int64_t to = a.row_slot ? a.row_slot[row] : row;
+      if (to >= 0 && to < a.n_slots) a.dw[to] = dot;
+    }
+  }
+}
+
+RowMap row_map(int cols) {
+  RowMap m;
+  m.steps = (uint32_t)(cols / kCols);
+  m.cpr8 = (m.steps + kQuad - 1) / kQuad * kQuad;
+  m.magic = ~uint64_t(0) / m.cpr8 + 1;
+  return m;
+}
+// Workgroups over `steps` steps of all rows (the live rows are only known on the device).
+unsigned grid_of(int64_t rows, const RowMap& m) {
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>((rows * m.cpr8 + kThreads - 1) / kThreads, 1 << 20));
+}
+
+}  // namespace
+
+hipError_t launch_act8_pack(int dtype, const void* x, int64_t ldx, const int32_t* n_rows, int64_t rows, int cols,
+                            void* codes, void* scales, hipStream_t s) {
+  const RowMap m = row_map(cols);
+  return with_rows(dtype, [&](auto* t) {
+    typedef std::remove_pointer_t<decltype(t)> XT;
+    act8_pack_kernel<XT><<<grid_of(rows, m), kThreads, 0, s>>>(static_cast<const XT*>(x), ldx, n_rows, rows, cols, m,
+                                                              static_cast<uint8_t*>(codes),
+                                                              static_cast<uint8_t*>(scales));
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_act8_unpack(int dtype, const void* codes, const void* scales, const int32_t* n_rows, int64_t rows,
+                              int cols, void* out, int64_t ldo, hipStream_t s) {
+  const RowMap m = row_map(cols);
+  return with_rows(dtype, [&](auto* t) {
+    typedef std::remove_pointer_t<decltype(t)> XT;
+    act8_unpack_kernel<XT><<<grid_of(rows, m), kThreads, 0, s>>>(
+        static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), n_rows, rows, cols, m,
+        static_cast<XT*>(out), ldo);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_swiglu_keep8(const SwigluKeep8Args& a, hipStream_t s) {
+  const RowMap m = row_map(a.F);
+  return with_rows(a.dtype, [&](auto* t) {
+    typedef std::remove_pointer_t<decltype(t)> XT;
+    swiglu_keep8_kernel<XT><<<grid_of(a.rows, m), kThreads, 0, s>>>(
+        static_cast<const XT*>(a.g), static_cast<const XT*>(a.u), a.ld, a.n_rows, a.rows, a.F, m,
+        static_cast<XT*>(a.h), static_cast<uint8_t*>(a.codes_g), static_cast<uint8_t*>(a.scales_g),
+        static_cast<uint8_t*>(a.codes_u), static_cast<uint8_t*>(a.scales_u));
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_swiglu_bwd8(const SwigluBwd8Args& a, hipStream_t s) {
+  const Bwd8 b{static_cast<const uint8_t*>(a.codes_g), static_cast<const uint8_t*>(a.scales_g),
+               static_cast<const uint8_t*>(a.codes_u), static_cast<const uint8_t*>(a.scales_u),
+               a.n_rows, a.w_rows, a.row_slot, a.dw, a.n_slots, a.rows, a.ld, a.F};
+  const RowMap m = row_map(a.F);
+  return with_rows(a.dh_dtype, [&](auto* t) {
+    return with_rows(a.out_dtype, [&](auto* o) {
+      typedef std::remove_pointer_t<decltype(t)> DT;
+      typedef std::remove_pointer_t<decltype(o)> OT;
+      const DT* dh = static_cast<const DT*>(a.dh);
+      OT *dg = static_cast<OT*>(a.dg), *du = static_cast<OT*>(a.du), *h = static_cast<OT*>(a.h);
+      if (a.dw) {
+        const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + 3) / 4, 1 << 20);
+        swiglu_bwd8_row_kernel<DT, OT><<<blocks, kThreads, 0, s>>>(b, dh, dg, du, h);
+      } else {
+        swiglu_bwd8_kernel<DT, OT><<<grid_of(a.rows, m), kThreads, 0, s>>>(b, m, dh, dg, du, h);
+      }
+      return hipGetLastError();
+    });
+  });
+}
+
+}  // namespace moe

@@ -364,6 +364,7 @@ size_t moe_workspace_bytes(const moe_dims* d, int32_t which) {
     case MOE_WS_PERMUTE: return permute_ws_bytes(d->T, d->n_experts);
     case MOE_WS_AUX: return aux_ws_bytes(d->n_experts, d->n_null);
     case MOE_WS_BACKWARD: return d->dtype == MOE_BF16 ? bwd_ws(d).total : 0;
+    case MOE_WS_COMBINE_BACKWARD: return combine_bwd_ws_bytes(d->T, d->d_model, d->null_kind);
   }
   return 0;
 }
@@ -540,6 +541,162 @@ moe_status moe_combine(const moe_dims* d, const void* y_perm, const int32_t* slo
   CombineArgs c{d->dtype == MOE_BF16, d->T, d->top_k, d->d_model, max_rows(d), y_perm, slot_pos,
                 topk_w, y_shared, d->null_kind != MOE_NULL_ZERO ? null_src : nullptr, null_stride(d), y};
   HIP_TRY(launch_combine(c, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+// Dispatch gradients and combine of rows in any storage type.
+static bool row_dtype(int32_t t) { return t == MOE_F32 || t == MOE_BF16 || t == MOE_F16; }
+static moe_status check_row_dims(const moe_dims* d, int32_t rows_dtype) {
+  MOE_TRY(check_dims(d));
+  if (!row_dtype(rows_dtype)) return MOE_ERR_ARG;
+  return d->d_model > (1 << 30) ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+moe_status moe_combine_rows(const moe_dims* d, int32_t rows_dtype, const void* y_perm, const int32_t* slot_pos,
+                            const float* topk_w, const void* y_shared, const void* null_src, void* y,
+                            moe_stream stream) {
+  MOE_TRY(check_row_dims(d, rows_dtype));
+  MOE_TRY(need(y_perm));
+  MOE_TRY(need(slot_pos));
+  MOE_TRY(need(topk_w));
+  MOE_TRY(maybe(y_shared));
+  if (d->null_kind != MOE_NULL_ZERO) MOE_TRY(need(null_src));
+  MOE_TRY(need(y));
+  if (d->T == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  const SlotSumArgs a{d->T, d->top_k, d->d_model, max_rows(d), rows_dtype, d->dtype, y_perm, slot_pos, topk_w,
+                      y_shared, d->null_kind != MOE_NULL_ZERO ? null_src : nullptr, null_stride(d), y};
+  HIP_TRY(launch_combine_rows(a, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_permute_backward(const moe_dims* d, int32_t rows_dtype, const void* dx_perm, const int32_t* slot_pos,
+                                const float* dx_add, int32_t dx_dtype, void* dx, moe_stream stream) {
+  MOE_TRY(check_row_dims(d, rows_dtype));
+  if (!row_dtype(dx_dtype) || (dx_add && dx_add == dx && dx_dtype != MOE_F32)) return MOE_ERR_ARG;
+  MOE_TRY(need(dx_perm));
+  MOE_TRY(need(slot_pos));
+  MOE_TRY(maybe(dx_add));
+  MOE_TRY(need(dx));
+  if (d->T == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  const SlotSumArgs a{d->T, d->top_k, d->d_model, max_rows(d), rows_dtype, dx_dtype, dx_perm, slot_pos, nullptr,
+                      dx_add, nullptr, 0, dx};
+  HIP_TRY(launch_permute_bwd(a, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_combine_backward(const moe_dims* d, int32_t rows_dtype, const void* dy, const void* y_perm,
+                                const int32_t* slot_pos, const float* topk_w, const void* null_src, void* dy_perm,
+                                float* w_perm, int32_t* row_slot, float* dtopk_w, float* dnull, void* ws,
+                                size_t ws_bytes, moe_stream stream) {
+  MOE_TRY(check_row_dims(d, rows_dtype));
+  MOE_TRY(need(dy));
+  MOE_TRY(maybe(y_perm));
+  MOE_TRY(need(slot_pos));
+  MOE_TRY(need(topk_w));
+  const bool null_row = d->null_kind != MOE_NULL_ZERO;
+  if (null_row) MOE_TRY(need(null_src));
+  MOE_TRY(maybe(dy_perm));
+  MOE_TRY(maybe(w_perm));
+  MOE_TRY(maybe(row_slot));
+  MOE_TRY(maybe(dtopk_w));
+  if (null_row) MOE_TRY(maybe(dnull));
+  const size_t need_ws = null_row && dnull ? combine_bwd_ws_bytes(d->T, d->d_model, d->null_kind) : 0;
+  if (need_ws) {
+    if (!ws || ws_bytes < need_ws) return MOE_ERR_WORKSPACE;
+    MOE_TRY(need(ws));
+  }
+  if (d->T == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  const CombineBwdArgs a{d->dtype == MOE_BF16, d->T, d->top_k, d->d_model, max_rows(d), rows_dtype, dy, y_perm,
+                         slot_pos, topk_w, null_row ? null_src : nullptr, null_stride(d), dy_perm, w_perm, row_slot,
+                         dtopk_w, null_row ? dnull : nullptr, static_cast<float*>(ws)};
+  HIP_TRY(launch_combine_bwd(a, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+// 8-bit activation checkpoints. The row count may be any element of an array (the last
+// of moe_permute's offsets), so it is held to its own alignment only.
+static moe_status maybe_count(const int32_t* n) {
+  return reinterpret_cast<uintptr_t>(n) & 3u ? MOE_ERR_ALIGN : MOE_OK;
+}
+static moe_status check_act8(int64_t rows, int32_t cols, int32_t dtype, int64_t ld) {
+  if (rows < 0 || cols < 8 || cols % 8 || !row_dtype(dtype) || ld < cols || ld % 8) return MOE_ERR_ARG;
+  if (rows >= (int64_t(1) << 40) || ld >= (int64_t(1) << 40) || rows * (double)ld >= 1099511627776.0)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_act8_pack(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ldx,
+                         const int32_t* n_rows, int8_t* codes, uint8_t* scales, moe_stream stream) {
+  MOE_TRY(check_act8(rows, cols, dtype, ldx));
+  MOE_TRY(need(x));
+  MOE_TRY(maybe_count(n_rows));
+  MOE_TRY(need(codes));
+  MOE_TRY(need(scales));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  HIP_TRY(launch_act8_pack(dtype, x, ldx, n_rows, rows, cols, codes, scales, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_act8_unpack(int64_t rows, int32_t cols, int32_t dtype, const int8_t* codes, const uint8_t* scales,
+                           const int32_t* n_rows, void* out, int64_t ldo, moe_stream stream) {
+  MOE_TRY(check_act8(rows, cols, dtype, ldo));
+  MOE_TRY(need(codes));
+  MOE_TRY(need(scales));
+  MOE_TRY(maybe_count(n_rows));
+  MOE_TRY(need(out));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  HIP_TRY(launch_act8_unpack(dtype, codes, scales, n_rows, rows, cols, out, ldo, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_swiglu_keep8(int64_t rows, int32_t d_ff, int32_t dtype, const void* g, const void* u, int64_t ld,
+                            const int32_t* n_rows, void* h, int8_t* codes_g, uint8_t* scales_g, int8_t* codes_u,
+                            uint8_t* scales_u, moe_stream stream) {
+  MOE_TRY(check_act8(rows, d_ff, dtype, ld));
+  MOE_TRY(need(g));
+  MOE_TRY(need(u));
+  MOE_TRY(maybe_count(n_rows));
+  MOE_TRY(need(h));
+  MOE_TRY(need(codes_g));
+  MOE_TRY(need(scales_g));
+  MOE_TRY(need(codes_u));
+  MOE_TRY(need(scales_u));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  const SwigluKeep8Args a{rows, d_ff, dtype, g, u, ld, n_rows, h, codes_g, scales_g, codes_u, scales_u};
+  HIP_TRY(launch_swiglu_keep8(a, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_g, const uint8_t* scales_g,
+                                const int8_t* codes_u, const uint8_t* scales_u, const int32_t* n_rows,
+                                int32_t dh_dtype, const void* dh, const float* w_rows, const int32_t* row_slot,
+                                int64_t n_slots, int32_t out_dtype, void* dg, void* du, int64_t ld, void* h,
+                                float* dw, moe_stream stream) {
+  MOE_TRY(check_act8(rows, d_ff, out_dtype, ld));
+  if (!row_dtype(dh_dtype) || (dw && n_slots < 0)) return MOE_ERR_ARG;
+  MOE_TRY(need(codes_g));
+  MOE_TRY(need(scales_g));
+  MOE_TRY(need(codes_u));
+  MOE_TRY(need(scales_u));
+  MOE_TRY(maybe_count(n_rows));
+  MOE_TRY(need(dh));
+  MOE_TRY(maybe(w_rows));
+  MOE_TRY(maybe(row_slot));
+  MOE_TRY(need(dg));
+  MOE_TRY(need(du));
+  MOE_TRY(maybe(h));
+  MOE_TRY(maybe(dw));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  const SwigluBwd8Args a{rows, d_ff, codes_g, scales_g, codes_u, scales_u, n_rows, dh_dtype, dh, w_rows, row_slot,
+                         n_slots, out_dtype, dg, du, ld, h, dw};
+  HIP_TRY(launch_swiglu_bwd8(a, static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 

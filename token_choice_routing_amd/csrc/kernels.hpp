@@ -234,6 +234,78 @@ struct CombineArgs {
 };
 hipError_t launch_combine(const CombineArgs& a, hipStream_t stream);
 
+// Slot sums (dispatch_grad.hip): y[t] = shared[t] + sum over slots of w rows[slot_pos],
+// null slots adding null_src; types are moe_dtype values.
+struct SlotSumArgs {
+  int64_t T;
+  int K, d;
+  int64_t max_rows;
+  int rows_dtype, out_dtype;
+  const void* rows;
+  const int32_t* slot_pos;
+  const float* topk_w;      // combine only
+  const void* shared;       // combine: rows_dtype; permute gradient: float32
+  const void* null_src;     // out_dtype rows a null slot adds, or NULL
+  int64_t null_stride;      // elements between the rows of consecutive tokens (0: one row)
+  void* y;
+};
+hipError_t launch_combine_rows(const SlotSumArgs& a, hipStream_t stream);  // out_dtype float32 or bf16
+hipError_t launch_permute_bwd(const SlotSumArgs& a, hipStream_t stream);   // every weight 1
+
+struct CombineBwdArgs {
+  bool bf16;                // dy and null_src
+  int64_t T;
+  int K, d;
+  int64_t max_rows;
+  int rows_dtype;
+  const void* dy;
+  const void* y_perm;       // or NULL: the real slots' dtopk_w is not written
+  const int32_t* slot_pos;
+  const float* topk_w;
+  const void* null_src;     // or NULL
+  int64_t null_stride;      // d: one row per token (copy), 0: one vector (constant)
+  void* dy_perm;            // every output may be NULL
+  float* w_perm;
+  int32_t* row_slot;
+  float* dtopk_w;
+  float* dnull;
+  float* part;              // combine_bwd_ws_bytes(T, d, null_kind) bytes
+};
+size_t combine_bwd_ws_bytes(int64_t T, int d, int null_kind);
+hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream);
+
+// 8-bit activation checkpoints (act8.hip).
+hipError_t launch_act8_pack(int dtype, const void* x, int64_t ldx, const int32_t* n_rows, int64_t rows, int cols,
+                            void* codes, void* scales, hipStream_t s);
+hipError_t launch_act8_unpack(int dtype, const void* codes, const void* scales, const int32_t* n_rows, int64_t rows,
+                              int cols, void* out, int64_t ldo, hipStream_t s);
+struct SwigluKeep8Args {
+  int64_t rows;
+  int F, dtype;
+  const void *g, *u;
+  int64_t ld;
+  const int32_t* n_rows;
+  void *h, *codes_g, *scales_g, *codes_u, *scales_u;
+};
+hipError_t launch_swiglu_keep8(const SwigluKeep8Args& a, hipStream_t s);
+struct SwigluBwd8Args {
+  int64_t rows;
+  int F;
+  const void *codes_g, *scales_g, *codes_u, *scales_u;
+  const int32_t* n_rows;
+  int dh_dtype;
+  const void* dh;
+  const float* w_rows;
+  const int32_t* row_slot;
+  int64_t n_slots;
+  int out_dtype;
+  void *dg, *du;
+  int64_t ld;
+  void* h;
+  float* dw;
+};
+hipError_t launch_swiglu_bwd8(const SwigluBwd8Args& a, hipStream_t s);
+
 struct AuxArgs {
   int64_t T;
   int N, M, K;

@@ -1,0 +1,86 @@
+// Rows of activations in the three storage types (float32, bf16, IEEE half): E
+// consecutive elements as float32 and back, one rounding to nearest even each.
+#pragma once
+#include "common.hpp"
+
+namespace moe {
+
+typedef _Float16 half_t;
+typedef half_t f16x4_t __attribute__((ext_vector_type(4)));
+
+// E = 4 or 8 elements at p (16-byte aligned rows, E-element aligned columns).
+template <int E>
+__device__ __forceinline__ void load_row(const float* p, float* v) {
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q) {
+    const f32x4_t a = *reinterpret_cast<const f32x4_t*>(p + 4 * q);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[4 * q + j] = a[j];
+  }
+}
+template <int E>
+__device__ __forceinline__ void load_row(const bf16_t* p, float* v) {
+  if constexpr (E == 8) {
+    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[2 * j] = __uint_as_float(a[j] << 16);
+      v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+    }
+  } else {
+    const u32x2_t a = *reinterpret_cast<const u32x2_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v[2 * j] = __uint_as_float(a[j] << 16);
+      v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
+    }
+  }
+}
+template <int E>
+__device__ __forceinline__ void load_row(const half_t* p, float* v) {
+  if constexpr (E == 8) {
+    const f16x8_t a = *reinterpret_cast<const f16x8_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
+  } else {
+    const f16x4_t a = *reinterpret_cast<const f16x4_t*>(p);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = (float)a[j];
+  }
+}
+
+template <int E>
+__device__ __forceinline__ void store_row(float* p, const float* v) {
+#pragma unroll
+  for (int q = 0; q < E / 4; ++q)
+    *reinterpret_cast<f32x4_t*>(p + 4 * q) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+}
+template <int E>
+__device__ __forceinline__ void store_row(bf16_t* p, const float* v) {
+  if constexpr (E == 8)
+    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  else
+    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+}
+template <int E>
+__device__ __forceinline__ void store_row(half_t* p, const float* v) {
+  if constexpr (E == 8)
+    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]),
+                                             pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7])};
+  else
+    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+}
+
+// Calls f with a null pointer of the element type that dtype (moe_dtype) names.
+template <typename F>
+hipError_t with_rows(int dtype, F&& f) {
+  switch (dtype) {
+    case MOE_F32: return f(static_cast<float*>(nullptr));
+    case MOE_BF16: return f(static_cast<bf16_t*>(nullptr));
+    case MOE_F16: return f(static_cast<half_t*>(nullptr));
+  }
+  return hipErrorInvalidValue;
+}
+
+}  // namespace moe
