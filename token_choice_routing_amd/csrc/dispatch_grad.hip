@@ -25,15 +25,23 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroup = 4;  // slots whose rows are loaded before the first is added
+constexpr int kCols = 8;   // columns per lane
+constexpr int kSpan = kWave * kCols;  // columns per wavefront
+// Slots whose rows are loaded before the first is used. Eight take the registers of
+// half the wavefronts (combine at 16384 x 2048, 8 slots a quarter real: 62 us against 53).
+constexpr int kGroup = 4;
 
 // Position of a slot: a row of y_perm, or what stands in for one.
 constexpr int kNullSlot = -1, kNoSlot = -2;
 
 // y[t] = shared[t] + sum over slots of w r, in slot order (fmaf, one rounding). One
-// wavefront per token and span of 64 E V columns; the token's positions and weights
-// are read once by lanes 0..K-1 and broadcast. WEIGHTED false: every weight is 1.
-template <typename RT, typename AT, typename ET, int E, int V, bool WEIGHTED>
+// wavefront per token and span of kSpan columns: the token's positions and weights are
+// read once by lanes 0..K-1 and broadcast, and every row's load is in flight before the
+// first is added. A wavefront with two or four spans of a token reads the positions less
+// often but holds fewer loads in flight over the chip (16384 x 2048, 8 slots a quarter
+// real, bf16: 50.7 us at 5.3 TB/s with one span, 52.8 with two, 73 with four).
+// WEIGHTED false: every weight is 1.
+template <typename RT, typename AT, typename ET, bool WEIGHTED>
 __global__ void __launch_bounds__(kThreads)
 slot_sum_kernel(const RT* __restrict__ rows, const int32_t* __restrict__ slot_pos,
                 const float* __restrict__ topk_w, const AT* shared, const ET* __restrict__ null_src,
@@ -44,7 +52,8 @@ slot_sum_kernel(const RT* __restrict__ rows, const int32_t* __restrict__ slot_po
   const int64_t units = T * spans;
   for (int64_t unit = wave; unit < units; unit += nwaves) {
     const int64_t t = unit / spans;
-    const int c0 = (int)(unit - t * spans) * (kWave * E * V) + lane * E;
+    const int c = (int)(unit - t * spans) * kSpan + lane * kCols;
+    const bool on = c < d;
     int my_p = kNoSlot;
     float my_w = 1.0f;
     if (lane < K) {
@@ -52,21 +61,18 @@ slot_sum_kernel(const RT* __restrict__ rows, const int32_t* __restrict__ slot_po
       if (WEIGHTED) my_w = topk_w[t * K + lane];
       if (my_p == kNullSlot ? !null_src : (my_p < 0 || my_p >= max_rows)) my_p = kNoSlot;
     }
-    float acc[V][E], nul[V][E];
+    float acc[kCols], nul[kCols];
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = c0 + v * kWave * E;
-#pragma unroll
-      for (int j = 0; j < E; ++j) acc[v][j] = nul[v][j] = 0.0f;
-      if (c < d) {
-        if (shared) load_row<E>(shared + t * d + c, acc[v]);
-        if (null_src) load_row<E>(null_src + t * null_stride + c, nul[v]);
-      }
+    for (int j = 0; j < kCols; ++j) acc[j] = nul[j] = 0.0f;
+    if (on) {
+      if (shared) load_row<kCols>(shared + t * d + c, acc);
+      if (null_src) load_row<kCols>(null_src + t * null_stride + c, nul);
     }
     uint64_t todo = ballot(my_p != kNoSlot);
     while (todo) {
       int p[kGroup];
-      float w[kGroup], r[kGroup][V][E];
+      float w[kGroup];
+      RawRow<RT, kCols> r[kGroup];
 #pragma unroll
       for (int g = 0; g < kGroup; ++g) {
         p[g] = kNoSlot;
@@ -75,231 +81,229 @@ slot_sum_kernel(const RT* __restrict__ rows, const int32_t* __restrict__ slot_po
           todo &= todo - 1;
           p[g] = __builtin_amdgcn_readlane(my_p, k);
           w[g] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), k));
-          if (p[g] >= 0) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-              const int c = c0 + v * kWave * E;
-              if (c < d) load_row<E>(rows + (int64_t)p[g] * d + c, r[g][v]);
-            }
-          }
+          if (p[g] >= 0 && on) r[g].load(rows + (int64_t)p[g] * d + c);
         }
       }
 #pragma unroll
       for (int g = 0; g < kGroup; ++g) {
-        if (p[g] == kNoSlot) continue;
+        if (p[g] >= 0) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
+          for (int j = 0; j < kCols; ++j)
+            acc[j] = WEIGHTED ? fmaf(w[g], r[g][j], acc[j]) : acc[j] + r[g][j];
+        } else if (p[g] == kNullSlot) {
 #pragma unroll
-          for (int j = 0; j < E; ++j) {
-            const float x = p[g] >= 0 ? r[g][v][j] : nul[v][j];
-            acc[v][j] = WEIGHTED ? fmaf(w[g], x, acc[v][j]) : acc[v][j] + x;
-          }
+          for (int j = 0; j < kCols; ++j) acc[j] = fmaf(w[g], nul[j], acc[j]);
+        }
       }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = c0 + v * kWave * E;
-      if (c < d) store_row<E>(y + t * d + c, acc[v]);
-    }
+    if (on) store_row<kCols>(y + t * d + c, acc);
   }
 }
 
+// Sum over the wavefront, the same in every lane: rows of 16 lanes by permutations
+// inside them, then the rows' sums passed up (lane 63 holds the total).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float add_dpp(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CTRL, ROWS, 0xF, false));
+}
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+  v = add_dpp<0xB1, 0xF>(v);   // lanes 1 0 3 2
+  v = add_dpp<0x4E, 0xF>(v);   // lanes 2 3 0 1
+  v = add_dpp<0x141, 0xF>(v);  // mirrored in halves of a row
+  v = add_dpp<0x140, 0xF>(v);  // mirrored in a row
+  v = add_dpp<0x142, 0xA>(v);  // lane 15 of rows 0, 2 into rows 1, 3
+  v = add_dpp<0x143, 0xC>(v);  // lane 31 into rows 2, 3
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 
-// The combine's gradient, one wavefront per token; V column vectors of E elements per
-// lane and pass. ONE: the row fits one pass, so dy_t stays in registers over the slots.
-template <typename RT, typename ET, int E, int V, bool ONE>
+// The combine's gradient: WPT wavefronts per token, each with every WPT-th span of
+// kSpan columns, whose parts of the slots' products meet in LDS. One wavefront per token
+// holds the whole row's loads in registers and so fewer of them over the chip (16384 x
+// 2048, 8 slots a quarter real, bf16: 106 us, 80 us with two slots at a time).
+template <typename RT, typename ET, int WPT>
 __global__ void __launch_bounds__(kThreads)
 combine_bwd_kernel(const ET* __restrict__ dy, const RT* __restrict__ y_perm, const int32_t* __restrict__ slot_pos,
                    const float* __restrict__ topk_w, const ET* __restrict__ null_src, int64_t null_stride,
                    RT* __restrict__ dy_perm, float* __restrict__ w_perm, int32_t* __restrict__ row_slot,
                    float* __restrict__ dtopk_w, float* __restrict__ dnull, int64_t T, int K, int d,
                    int64_t max_rows) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int64_t nwaves = (int64_t)gridDim.x * (kThreads / kWave);
-  const int span = kWave * E * V;
-  for (int64_t t = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; t < T; t += nwaves) {
+  constexpr int kTokens = kThreads / kWave / WPT;  // tokens per workgroup
+  __shared__ float part[kThreads / kWave][MOE_MAX_TOPK];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, sub = wave % WPT;
+  const bool dots = y_perm && dtopk_w;
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < T; t0 += (int64_t)gridDim.x * kTokens) {
+    const int64_t t = t0 + wave / WPT;
     int my_p = kNoSlot;
-    float my_w = 0.0f;
-    if (lane < K) {
+    float my_w = 0.0f, my_dot = 0.0f;  // lane k: slot k
+    if (t < T && lane < K) {
       my_p = slot_pos[t * K + lane];
       my_w = topk_w[t * K + lane];
       if (my_p != kNullSlot && (my_p < 0 || my_p >= max_rows)) my_p = kNoSlot;
-      if (my_p >= 0) {
+      if (my_p >= 0 && sub == 0) {
         if (w_perm) w_perm[my_p] = my_w;
         if (row_slot) row_slot[my_p] = (int32_t)(t * K + lane);
       }
     }
-    float my_dot = 0.0f;  // lane k: the weight gradient of slot k
-    const uint64_t nulls = ballot(my_p == kNullSlot);
-    const ET* dyt = dy + t * d;
-    float g[V][E];
-    auto load_dy = [&](int c0) {
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const int c = c0 + v * kWave * E + lane * E;
-#pragma unroll
-        for (int j = 0; j < E; ++j) g[v][j] = 0.0f;
-        if (c < d) load_row<E>(dyt + c, g[v]);
-      }
-    };
-    if (ONE) load_dy(0);
-    // the expert rows, kGroup slots at a time
-    uint64_t todo = ballot(my_p >= 0);
-    while (todo && (dy_perm || (y_perm && dtopk_w))) {
-      int p[kGroup], k[kGroup];
-      float w[kGroup], dot[kGroup];
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        p[i] = kNoSlot;
-        k[i] = 0;
-        w[i] = dot[i] = 0.0f;
-        if (todo) {
-          k[i] = __builtin_ctzll(todo);
-          todo &= todo - 1;
-          p[i] = __builtin_amdgcn_readlane(my_p, k[i]);
-          w[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), k[i]));
-        }
-      }
-      for (int c0 = 0; c0 < d; c0 += span) {
-        if (!ONE) load_dy(c0);
-#pragma unroll
-        for (int i = 0; i < kGroup; ++i) {
-          if (p[i] < 0) continue;
-#pragma unroll
-          for (int v = 0; v < V; ++v) {
-            const int c = c0 + v * kWave * E + lane * E;
-            if (c >= d) continue;
-            if (y_perm && dtopk_w) {
-              float r[E];
-              load_row<E>(y_perm + (int64_t)p[i] * d + c, r);
-#pragma unroll
-              for (int j = 0; j < E; ++j) dot[i] = fmaf(g[v][j], r[j], dot[i]);
-            }
-            if (dy_perm) {
-              float o[E];
-#pragma unroll
-              for (int j = 0; j < E; ++j) o[j] = w[i] * g[v][j];
-              store_row<E>(dy_perm + (int64_t)p[i] * d + c, o);
-            }
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kGroup; ++i) {
-        const float s = wave_sum(dot[i]);
-        if (p[i] >= 0 && lane == k[i]) my_dot = s;
-      }
-    }
-    // the null slots: one product <dy_t, null source> for all of them, and the copied
-    // token's gradient (sum of their weights) dy_t
-    if (null_src && nulls && (dtopk_w || dnull)) {
-      float wn = 0.0f;
+    const uint64_t reals = ballot(my_p >= 0), nulls = ballot(my_p == kNullSlot);
+    float wn = 0.0f;  // sum of the null slots' weights
+    if (dnull)
       for (uint64_t m = nulls; m; m &= m - 1)
         wn += __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), __builtin_ctzll(m)));
-      float dot = 0.0f;
-      for (int c0 = 0; c0 < d; c0 += span) {
-        if (!ONE) load_dy(c0);
+    for (int c0 = sub * kSpan; t < T && c0 < d; c0 += WPT * kSpan) {
+      const int c = c0 + lane * kCols;
+      const bool on = c < d;
+      RawRow<ET, kCols> g, nul;
+      g.zero();
+      nul.zero();
+      if (on) g.load(dy + t * d + c);
+      const bool null_dot = null_src && dtopk_w && nulls;
+      if (null_dot && on) nul.load(null_src + t * null_stride + c);
+      // the expert rows, kGroup slots at a time
+      for (uint64_t todo = dy_perm || dots ? reals : 0; todo;) {
+        int p[kGroup], k[kGroup];
+        float w[kGroup];
+        RawRow<RT, kCols> r[kGroup];
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const int c = c0 + v * kWave * E + lane * E;
-          if (c >= d) continue;
-          if (dtopk_w) {
-            float r[E];
-            load_row<E>(null_src + t * null_stride + c, r);
-#pragma unroll
-            for (int j = 0; j < E; ++j) dot = fmaf(g[v][j], r[j], dot);
+        for (int i = 0; i < kGroup; ++i) {
+          p[i] = kNoSlot;
+          r[i].zero();
+          if (todo) {
+            k[i] = __builtin_ctzll(todo);
+            todo &= todo - 1;
+            p[i] = __builtin_amdgcn_readlane(my_p, k[i]);
+            w[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), k[i]));
+            if (dots && on) r[i].load(y_perm + (int64_t)p[i] * d + c);
           }
-          if (dnull) {
-            float o[E];
+        }
+        if (dy_perm && on) {
 #pragma unroll
-            for (int j = 0; j < E; ++j) o[j] = wn * g[v][j];
-            store_row<E>(dnull + t * d + c, o);
+          for (int i = 0; i < kGroup; ++i) {
+            if (p[i] < 0) continue;
+            float o[kCols];
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) o[j] = w[i] * g[j];
+            store_row<kCols>(dy_perm + (int64_t)p[i] * d + c, o);
+          }
+        }
+        if (dots) {
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) {
+            if (p[i] < 0) continue;
+            float dot = 0.0f;
+#pragma unroll
+            for (int j = 0; j < kCols; ++j) dot = fmaf(g[j], r[i][j], dot);
+            dot = wave_sum(dot);
+            if (lane == k[i]) my_dot += dot;
           }
         }
       }
-      dot = wave_sum(dot);
-      if (my_p == kNullSlot) my_dot = dot;
-    } else if (dnull) {  // no null slot: the copied token gets nothing
-      for (int c = lane * E; c < d; c += kWave * E) {
-        float o[E];
+      // the null slots share one product; the copied token gets their weights' sum times dy
+      if (null_dot) {
+        float dot = 0.0f;
 #pragma unroll
-        for (int j = 0; j < E; ++j) o[j] = 0.0f;
-        store_row<E>(dnull + t * d + c, o);
+        for (int j = 0; j < kCols; ++j) dot = fmaf(g[j], nul[j], dot);
+        dot = wave_sum(dot);
+        if (my_p == kNullSlot) my_dot += dot;
+      }
+      if (dnull && on) {
+        float o[kCols];
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) o[j] = nulls ? wn * g[j] : 0.0f;
+        store_row<kCols>(dnull + t * d + c, o);
       }
     }
-    if (dtopk_w && lane < K && (y_perm || my_p < 0)) dtopk_w[t * K + lane] = my_dot;
+    if (!dtopk_w) continue;
+    if (WPT > 1) {
+      if (lane < MOE_MAX_TOPK) part[wave][lane] = my_dot;
+      __syncthreads();
+      if (sub == 0 && lane < K)
+        for (int i = 1; i < WPT; ++i) my_dot += part[wave + i][lane];
+      __syncthreads();
+    }
+    if (t < T && sub == 0 && lane < K && (y_perm || my_p < 0)) dtopk_w[t * K + lane] = my_dot;
   }
 }
 
 // Gradient of the constant null expert's vector, sum over tokens of (sum of the null
-// slots' weights) dy_t: float32 partial sums over chunks of kNullChunk tokens, then a
-// float64 sum of the partials in chunk order.
-constexpr int kNullChunk = 64;
+// slots' weights) dy_t: float32 sums over chunks of tokens, one wavefront per chunk and
+// 256 columns, then a float64 sum of the chunks in a fixed order. Short chunks for few
+// tokens keep the chip busy, longer ones for many keep the partial sums small next to dy.
+constexpr int kNullCols = 4;
+constexpr int kMaxNullChunk = 64;
+constexpr int null_chunk(int64_t T) { return T <= 4096 ? 16 : kMaxNullChunk; }
 template <typename ET>
 __global__ void __launch_bounds__(kThreads)
 null_vector_partial_kernel(const ET* __restrict__ dy, const int32_t* __restrict__ slot_pos,
-                           const float* __restrict__ topk_w, int64_t T, int K, int d, int64_t chunks,
+                           const float* __restrict__ topk_w, int64_t T, int K, int d, int chunk, int64_t chunks,
                            float* __restrict__ part) {
-  __shared__ float wn[kNullChunk];
-  __shared__ int has[kNullChunk];
-  for (int64_t chunk = blockIdx.x; chunk < chunks; chunk += gridDim.x) {
-    const int64_t t0 = chunk * kNullChunk;
-    const int n = (int)min<int64_t>(kNullChunk, T - t0);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-      float s = 0.0f;
-      int any = 0;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int spans = (d + kWave * kNullCols - 1) / (kWave * kNullCols);
+  const int64_t nwaves = (int64_t)gridDim.x * (kThreads / kWave);
+  for (int64_t unit = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; unit < chunks * spans;
+       unit += nwaves) {
+    const int64_t at = unit / spans, t0 = at * chunk;
+    const int n = (int)min<int64_t>(chunk, T - t0);
+    const int c = (int)(unit - at * spans) * kWave * kNullCols + lane * kNullCols;
+    float my_w = 0.0f;  // lane i: token t0 + i
+    bool any = false;
+    if (lane < n)
       for (int k = 0; k < K; ++k)
-        if (slot_pos[(t0 + i) * K + k] == kNullSlot) {
-          s += topk_w[(t0 + i) * K + k];
-          any = 1;
+        if (slot_pos[(t0 + lane) * K + k] == kNullSlot) {
+          my_w += topk_w[(t0 + lane) * K + k];
+          any = true;
         }
-      wn[i] = s;
-      has[i] = any;
-    }
-    __syncthreads();
-    for (int64_t c = ((int64_t)blockIdx.y * kThreads + threadIdx.x) * 4; c < d;
-         c += (int64_t)gridDim.y * kThreads * 4) {
-      float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      for (int i = 0; i < n; ++i) {
-        if (!has[i]) continue;
-        float g[4];
-        load_row<4>(dy + (t0 + i) * d + c, g);
+    float acc[kNullCols] = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kAhead = 8;
+    for (uint64_t todo = ballot(any); todo;) {
+      RawRow<ET, kNullCols> g[kAhead];
+      float w[kAhead];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = fmaf(wn[i], g[j], acc[j]);
+      for (int i = 0; i < kAhead; ++i) {
+        w[i] = 0.0f;
+        g[i].zero();
+        if (todo) {
+          const int k = __builtin_ctzll(todo);
+          todo &= todo - 1;
+          w[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), k));
+          if (c < d) g[i].load(dy + (t0 + k) * d + c);
+        }
       }
-      store_row<4>(part + chunk * d + c, acc);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int j = 0; j < kNullCols; ++j) acc[j] = fmaf(w[i], g[i][j], acc[j]);
     }
+    if (c < d) store_row<kNullCols>(part + at * d + c, acc);
   }
 }
-__global__ void __launch_bounds__(kThreads)
+// 64 columns per workgroup, chunks over its 16 wavefronts.
+constexpr int kReduceWaves = 16;
+__global__ void __launch_bounds__(kReduceWaves * kWave)
 null_vector_reduce_kernel(const float* __restrict__ part, int64_t chunks, int d, float* __restrict__ dnull) {
-  const int64_t c = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (c >= d) return;
+  __shared__ double sum[kReduceWaves][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave;
+  const int64_t c = (int64_t)blockIdx.x * kWave + lane;
   double s = 0.0;
-  for (int64_t i = 0; i < chunks; ++i) s += part[i * d + c];
-  dnull[c] = (float)s;
+  if (c < d) {
+#pragma unroll 8
+    for (int64_t i = wave; i < chunks; i += kReduceWaves) s += part[i * d + c];
+  }
+  sum[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && c < d) {
+    for (int i = 1; i < kReduceWaves; ++i) s += sum[i][lane];
+    dnull[c] = (float)s;
+  }
 }
 
 template <typename RT, typename AT, typename ET, bool WEIGHTED>
 hipError_t slot_sum(const SlotSumArgs& a, hipStream_t stream) {
-  constexpr int E = 8;
-  const int vectors = (a.d + kWave * E - 1) / (kWave * E);  // of one wavefront, per row
-  auto go = [&](auto v) {
-    constexpr int V = decltype(v)::value;
-    const int spans = (vectors + V - 1) / V;
-    const int64_t blocks = std::min<int64_t>((a.T * spans + 3) / 4, 1 << 20);
-    slot_sum_kernel<RT, AT, ET, E, V, WEIGHTED><<<(unsigned)blocks, kThreads, 0, stream>>>(
-        static_cast<const RT*>(a.rows), a.slot_pos, a.topk_w, static_cast<const AT*>(a.shared),
-        static_cast<const ET*>(a.null_src), a.null_stride, static_cast<ET*>(a.y), a.T, a.K, a.d, a.max_rows, spans);
-    return hipGetLastError();
-  };
-  return go(std::integral_constant<int, 2>{});
+  const int spans = (a.d + kSpan - 1) / kSpan;
+  const int64_t blocks = std::min<int64_t>((a.T * spans + 3) / 4, 1 << 20);
+  slot_sum_kernel<RT, AT, ET, WEIGHTED><<<(unsigned)blocks, kThreads, 0, stream>>>(
+      static_cast<const RT*>(a.rows), a.slot_pos, a.topk_w, static_cast<const AT*>(a.shared),
+      static_cast<const ET*>(a.null_src), a.null_stride, static_cast<ET*>(a.y), a.T, a.K, a.d, a.max_rows, spans);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -323,7 +327,8 @@ hipError_t launch_permute_bwd(const SlotSumArgs& a, hipStream_t stream) {
 }
 
 size_t combine_bwd_ws_bytes(int64_t T, int d, int null_kind) {
-  return null_kind == MOE_NULL_CONSTANT ? (size_t)((T + kNullChunk - 1) / kNullChunk) * d * sizeof(float) : 0;
+  const int64_t chunk = null_chunk(T);
+  return null_kind == MOE_NULL_CONSTANT ? (size_t)((T + chunk - 1) / chunk) * d * sizeof(float) : 0;
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
@@ -331,28 +336,29 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
   auto typed = [&](auto* r, auto* e) {
     typedef std::remove_pointer_t<decltype(r)> RT;
     typedef std::remove_pointer_t<decltype(e)> ET;
-    constexpr int E = 8;
-    const unsigned blocks = (unsigned)std::min<int64_t>((a.T + 3) / 4, 1 << 20);
     float* dnull = a.null_stride ? a.dnull : nullptr;  // per token; the constant's follows
-    auto go = [&](auto kernel) {
-      kernel<<<blocks, kThreads, 0, stream>>>(
+    auto go = [&](auto wpt) {
+      constexpr int WPT = decltype(wpt)::value, kTokens = kThreads / kWave / WPT;
+      const unsigned blocks = (unsigned)std::min<int64_t>((a.T + kTokens - 1) / kTokens, 1 << 20);
+      combine_bwd_kernel<RT, ET, WPT><<<blocks, kThreads, 0, stream>>>(
           static_cast<const ET*>(a.dy), static_cast<const RT*>(a.y_perm), a.slot_pos, a.topk_w,
           static_cast<const ET*>(a.null_src), a.null_stride, static_cast<RT*>(a.dy_perm), a.w_perm, a.row_slot,
           a.dtopk_w, dnull, a.T, a.K, a.d, a.max_rows);
     };
-    if (a.d <= 2 * kWave * E) go(combine_bwd_kernel<RT, ET, E, 2, true>);
-    else if (a.d <= 4 * kWave * E) go(combine_bwd_kernel<RT, ET, E, 4, true>);
-    else go(combine_bwd_kernel<RT, ET, E, 4, false>);
+    if (a.d <= kSpan) go(std::integral_constant<int, 1>{});
+    else if (a.d <= 2 * kSpan) go(std::integral_constant<int, 2>{});
+    else go(std::integral_constant<int, 4>{});
     hipError_t err = hipGetLastError();
     if (err != hipSuccess || !a.dnull || a.null_stride) return err;
-    const int64_t chunks = (a.T + kNullChunk - 1) / kNullChunk;
-    const dim3 grid((unsigned)std::min<int64_t>(chunks, 1 << 16),
-                    (unsigned)std::min<int64_t>(((int64_t)a.d + 4 * kThreads - 1) / (4 * kThreads), 64));
-    null_vector_partial_kernel<ET><<<grid, kThreads, 0, stream>>>(static_cast<const ET*>(a.dy), a.slot_pos, a.topk_w,
-                                                                  a.T, a.K, a.d, chunks, a.part);
+    const int chunk = null_chunk(a.T);
+    const int64_t chunks = (a.T + chunk - 1) / chunk;
+    const int spans = (a.d + kWave * kNullCols - 1) / (kWave * kNullCols);
+    null_vector_partial_kernel<ET><<<(unsigned)std::min<int64_t>((chunks * spans + 3) / 4, 1 << 20), kThreads, 0,
+                                     stream>>>(static_cast<const ET*>(a.dy), a.slot_pos, a.topk_w, a.T, a.K, a.d,
+                                               chunk, chunks, a.part);
     if ((err = hipGetLastError()) != hipSuccess) return err;
-    null_vector_reduce_kernel<<<(unsigned)((a.d + kThreads - 1) / kThreads), kThreads, 0, stream>>>(a.part, chunks,
-                                                                                                  a.d, a.dnull);
+    null_vector_reduce_kernel<<<(unsigned)((a.d + kWave - 1) / kWave), kReduceWaves * kWave, 0, stream>>>(
+        a.part, chunks, a.d, a.dnull);
     return hipGetLastError();
   };
   return with_rows(a.rows_dtype, [&](auto* r) {

@@ -1,6 +1,8 @@
 // Rows of activations in the three storage types (float32, bf16, IEEE half): E
 // consecutive elements as float32 and back, one rounding to nearest even each.
 #pragma once
+#include <type_traits>
+
 #include "common.hpp"
 
 namespace moe {
@@ -71,6 +73,25 @@ __device__ __forceinline__ void store_row(half_t* p, const float* v) {
   else
     *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
 }
+
+// E consecutive elements as loaded, converted where they are used: a load whose result
+// is converted inside a conditional block would be waited for in that block.
+template <typename T, int E>
+struct RawRow {
+  typedef uint32_t vec_t __attribute__((ext_vector_type(E * sizeof(T) / 4)));
+  vec_t v;
+  __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const vec_t*>(p); }
+  __device__ __forceinline__ void zero() { v = vec_t(0); }
+  __device__ __forceinline__ float operator[](int j) const {
+    if constexpr (sizeof(T) == 4) {
+      return __uint_as_float(v[j]);
+    } else {
+      const uint32_t w = v[j >> 1];
+      if constexpr (std::is_same<T, bf16_t>::value) return __uint_as_float(j & 1 ? w & 0xffff0000u : w << 16);
+      return (float)__builtin_bit_cast(f16x2_t, w)[j & 1];
+    }
+  }
+};
 
 // Calls f with a null pointer of the element type that dtype (moe_dtype) names.
 template <typename F>
