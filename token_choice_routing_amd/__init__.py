@@ -151,45 +151,63 @@ _DTYPES = {v: k for k, v in _ROW_TYPES.items()}
 _EMPTY = 256  # address of a tensor without elements (torch has none): nothing of it is accessed
 
 
-def _arg(name, t, dtype=None, shape=None, optional=False):
-    """Device address of a tensor argument whose type and shape the call fixes. The
-    library sees addresses only, so a tensor of another type, a smaller one or one on
-    another device than the current one is refused here (an int is taken as an address
-    as is)."""
+# The calls below move rows and often take microseconds on the device, so their
+# arguments are checked in few steps: one device query per call, and per tensor one test
+# that passes for a right argument; what is wrong is worked out only when it fails.
+
+def _device():
+    """Index of the current device; tensors of these calls have to be on it."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+
+
+def _row_stream(stream, dev):
+    """The stream of a call on device dev (torch's current one by default)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _refuse(name, t, dev, dtype, shape):
     if t is None:
-        if optional:
-            return None
         raise ValueError(f"{name} is required")
-    if isinstance(t, int):
-        return t
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: expected a tensor on the current device, got one on {t.device}")
-    if dtype is not None and t.dtype != dtype:
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: expected a tensor on the current device (cuda:{dev}), got one on {t.device}")
+    if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr() if t.numel() else _EMPTY
+    raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-def _matrix(name, t, dtype=None, shape=None):
+def _arg(name, t, dev, dtype, shape=None):
+    """Device address of a dense tensor whose type and shape the call fixes: the library
+    sees addresses only, so another type, shape or device is refused here."""
+    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
+            and (shape is None or t.shape == shape) and t.is_contiguous()):
+        _refuse(name, t, dev, dtype, shape)
+    return t.data_ptr() or _EMPTY
+
+
+def _opt(name, t, dev, dtype, shape=None):
+    return None if t is None else _arg(name, t, dev, dtype, shape)
+
+
+def _matrix(name, t, dev, dtype=None, shape=None):
     """(device address, elements from row to row) of a [rows][cols] tensor whose rows may
     be spaced (a column range of a wider matrix) but are dense inside."""
-    if t is None:
-        raise ValueError(f"{name} is required")
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: expected a tensor on the current device, got one on {t.device}")
-    if t.dim() != 2 or t.dtype not in _ROW_TYPES or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name}: expected a matrix of {dtype or 'float32, bfloat16 or float16'}, got "
-                         f"{tuple(t.shape)} of {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t is None or t.dim() != 2 or t.dtype not in _ROW_TYPES:
+        raise ValueError(f"{name}: expected a matrix of float32, bfloat16 or float16")
+    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype) or (shape is not None and t.shape != shape):
+        _refuse(name, t, dev, dtype or t.dtype, shape)
+    if t.is_contiguous():
+        return t.data_ptr() or _EMPTY, t.shape[1]
     rows, cols = t.shape
     ld = t.stride(0) if rows > 1 else cols
     if (cols > 1 and t.stride(1) != 1) or ld < cols:
         raise ValueError(f"{name}: expected rows that are dense and do not overlap, got strides {t.stride()}")
-    return (t.data_ptr() if t.numel() else _EMPTY), ld
+    return t.data_ptr() or _EMPTY, ld
 
 
 def _row_dtype(name, code):
@@ -287,23 +305,24 @@ def moe_combine(dims, y_perm, slot_pos, topk_w, y_shared, y, stream=None, null_s
 
 
 def _slot_shapes(dims):
-    """(dims dtype, [T][d], slot shape [T][K], rows in expert order) of a dispatch call."""
-    T, K, d = dims.T, dims.top_k, dims.d_model
-    return _DTYPES.get(dims.dtype), (T, d), (T, K), T * min(K, dims.n_experts)
+    """(dims dtype, [T][d], slots [T][K], rows in expert order, null source) of a dispatch call."""
+    T, K, d, N = dims.T, dims.top_k, dims.d_model, dims.n_experts
+    return (_DTYPES.get(dims.dtype), (T, d), (T, K), (T * (K if K < N else N), d),
+            (d,) if dims.null_kind == MOE_NULL_CONSTANT else (T, d))
 
 
 def moe_combine_rows(dims, rows_dtype, y_perm, slot_pos, topk_w, y_shared, y, null_src=None, stream=None):
     """moe_combine with y_perm and y_shared of type rows_dtype (MOE_F32, MOE_BF16 or
     MOE_F16). null_src: the rows a null slot adds (x for copy experts, v for constant)."""
-    dt, token, slots, cap = _slot_shapes(dims)
+    dev, f32 = _device(), torch.float32
+    dt, token, slots, rows, nul = _slot_shapes(dims)
     rt = _row_dtype("rows_dtype", rows_dtype)
-    nul = (dims.d_model,) if dims.null_kind == MOE_NULL_CONSTANT else token
     _check(load_library().moe_combine_rows(
-        ctypes.byref(dims), rows_dtype, _arg("y_perm", y_perm, rt, (cap, dims.d_model)),
-        _arg("slot_pos", slot_pos, torch.int32, slots), _arg("topk_w", topk_w, torch.float32, slots),
-        _arg("y_shared", y_shared, rt, token, True),
-        _arg("null_src", null_src, dt, nul, True) if dims.null_kind != MOE_NULL_ZERO else None,
-        _arg("y", y, dt, token), _stream(stream)), "moe_combine_rows")
+        ctypes.byref(dims), rows_dtype, _arg("y_perm", y_perm, dev, rt, rows),
+        _arg("slot_pos", slot_pos, dev, torch.int32, slots), _arg("topk_w", topk_w, dev, f32, slots),
+        _opt("y_shared", y_shared, dev, rt, token),
+        _opt("null_src", null_src, dev, dt, nul) if dims.null_kind else None,
+        _arg("y", y, dev, dt, token), _row_stream(stream, dev)), "moe_combine_rows")
 
 
 def moe_combine_backward(dims, rows_dtype, dy, y_perm, slot_pos, topk_w, dy_perm=None, w_perm=None, row_slot=None,
@@ -312,29 +331,30 @@ def moe_combine_backward(dims, rows_dtype, dy, y_perm, slot_pos, topk_w, dy_perm
     null source's dnull; w_perm and row_slot hold each expert row's weight and flat slot
     index. Every output is optional. ws: MOE_WS_COMBINE_BACKWARD bytes (constant nulls
     with dnull)."""
-    dt, token, slots, cap = _slot_shapes(dims)
-    rt, f32 = _row_dtype("rows_dtype", rows_dtype), torch.float32
-    nul = (dims.d_model,) if dims.null_kind == MOE_NULL_CONSTANT else token
+    dev, f32, i32 = _device(), torch.float32, torch.int32
+    dt, token, slots, rows, nul = _slot_shapes(dims)
+    rt = _row_dtype("rows_dtype", rows_dtype)
     null = dims.null_kind != MOE_NULL_ZERO
     wp, wb = _ws(ws)
     _check(load_library().moe_combine_backward(
-        ctypes.byref(dims), rows_dtype, _arg("dy", dy, dt, token),
-        _arg("y_perm", y_perm, rt, (cap, dims.d_model), True), _arg("slot_pos", slot_pos, torch.int32, slots),
-        _arg("topk_w", topk_w, f32, slots), _arg("null_src", null_src, dt, nul, True) if null else None,
-        _arg("dy_perm", dy_perm, rt, (cap, dims.d_model), True), _arg("w_perm", w_perm, f32, (cap,), True),
-        _arg("row_slot", row_slot, torch.int32, (cap,), True), _arg("dtopk_w", dtopk_w, f32, slots, True),
-        _arg("dnull", dnull, f32, nul, True) if null else None, wp, wb, _stream(stream)), "moe_combine_backward")
+        ctypes.byref(dims), rows_dtype, _arg("dy", dy, dev, dt, token), _opt("y_perm", y_perm, dev, rt, rows),
+        _arg("slot_pos", slot_pos, dev, i32, slots), _arg("topk_w", topk_w, dev, f32, slots),
+        _opt("null_src", null_src, dev, dt, nul) if null else None, _opt("dy_perm", dy_perm, dev, rt, rows),
+        _opt("w_perm", w_perm, dev, f32, rows[:1]), _opt("row_slot", row_slot, dev, i32, rows[:1]),
+        _opt("dtopk_w", dtopk_w, dev, f32, slots), _opt("dnull", dnull, dev, f32, nul) if null else None,
+        wp, wb, _row_stream(stream, dev)), "moe_combine_backward")
 
 
 def moe_permute_backward(dims, rows_dtype, dx_perm, slot_pos, dx_add, dx_dtype, dx, stream=None):
     """Gradient of moe_permute's gather: dx = dx_add (float32, optional) + the sum of each
     token's real rows of dx_perm (rows_dtype), in dx_dtype; dx may be dx_add itself."""
-    _, token, slots, cap = _slot_shapes(dims)
+    dev = _device()
+    _, token, slots, rows, _ = _slot_shapes(dims)
     rt, dt = _row_dtype("rows_dtype", rows_dtype), _row_dtype("dx_dtype", dx_dtype)
     _check(load_library().moe_permute_backward(
-        ctypes.byref(dims), rows_dtype, _arg("dx_perm", dx_perm, rt, (cap, dims.d_model)),
-        _arg("slot_pos", slot_pos, torch.int32, slots), _arg("dx_add", dx_add, torch.float32, token, True),
-        dx_dtype, _arg("dx", dx, dt, token), _stream(stream)), "moe_permute_backward")
+        ctypes.byref(dims), rows_dtype, _arg("dx_perm", dx_perm, dev, rt, rows),
+        _arg("slot_pos", slot_pos, dev, torch.int32, slots), _opt("dx_add", dx_add, dev, torch.float32, token),
+        dx_dtype, _arg("dx", dx, dev, dt, token), _row_stream(stream, dev)), "moe_permute_backward")
 
 
 ACT8_BLOCK = 32  # columns that share a scale byte
@@ -345,45 +365,48 @@ def act8_scales_shape(rows, cols):
     return rows, -(-cols // ACT8_BLOCK)
 
 
-def _kept(name, rows, cols, codes, scales):
-    return (_arg(f"{name}codes", codes, torch.int8, (rows, cols)),
-            _arg(f"{name}scales", scales, torch.uint8, act8_scales_shape(rows, cols)))
-
-
-def _live(n_rows):
-    return _arg("n_rows", n_rows, torch.int32, (1,), True)
+def _kept(dev, shape, codes, scales, name=""):
+    return (_arg(name + "codes", codes, dev, torch.int8, shape),
+            _arg(name + "scales", scales, dev, torch.uint8, (shape[0], -(-shape[1] // ACT8_BLOCK))))
 
 
 def moe_act8_pack(x, codes, scales, n_rows=None, stream=None):
     """8-bit checkpoint of x [rows][cols] (float32, bfloat16 or float16; rows may be
     spaced): codes int8 [rows][cols], scales uint8 [rows][ceil(cols / 32)]. n_rows: device
     int32 [1], the rows in use (all if None); the others are left as they were."""
-    px, ld = _matrix("x", x)
-    rows, cols = x.shape
-    _check(load_library().moe_act8_pack(rows, cols, _ROW_TYPES[x.dtype], px, ld, _live(n_rows),
-                                        *_kept("", rows, cols, codes, scales), _stream(stream)), "moe_act8_pack")
+    dev = _device()
+    px, ld = _matrix("x", x, dev)
+    shape = x.shape
+    pc, ps = _kept(dev, shape, codes, scales)
+    _check(load_library().moe_act8_pack(shape[0], shape[1], _ROW_TYPES[x.dtype], px, ld,
+                                        _opt("n_rows", n_rows, dev, torch.int32, (1,)), pc, ps,
+                                        _row_stream(stream, dev)), "moe_act8_pack")
 
 
 def moe_act8_unpack(codes, scales, out, n_rows=None, stream=None):
     """The values a checkpoint stands for, into out [rows][cols] (rows may be spaced)."""
-    po, ld = _matrix("out", out)
-    rows, cols = out.shape
-    _check(load_library().moe_act8_unpack(rows, cols, _ROW_TYPES[out.dtype], *_kept("", rows, cols, codes, scales),
-                                          _live(n_rows), po, ld, _stream(stream)), "moe_act8_unpack")
+    dev = _device()
+    po, ld = _matrix("out", out, dev)
+    shape = out.shape
+    pc, ps = _kept(dev, shape, codes, scales)
+    _check(load_library().moe_act8_unpack(shape[0], shape[1], _ROW_TYPES[out.dtype], pc, ps,
+                                          _opt("n_rows", n_rows, dev, torch.int32, (1,)), po, ld,
+                                          _row_stream(stream, dev)), "moe_act8_unpack")
 
 
 def moe_swiglu_keep8(g, u, h, g_codes, g_scales, u_codes, u_scales, n_rows=None, stream=None):
     """h = silu(g) u and the 8-bit checkpoints of g and u. g, u: [rows][d_ff] of one type,
     with the same spacing of rows; h: dense, the same type."""
-    pg, ld = _matrix("g", g)
-    pu, ldu = _matrix("u", u, g.dtype, g.shape)
-    rows, F = g.shape
+    dev = _device()
+    pg, ld = _matrix("g", g, dev)
+    shape, dt = g.shape, g.dtype
+    pu, ldu = _matrix("u", u, dev, dt, shape)
     if ld != ldu:
         raise ValueError(f"g and u: expected the same spacing of rows, got {ld} and {ldu}")
     _check(load_library().moe_swiglu_keep8(
-        rows, F, _ROW_TYPES[g.dtype], pg, pu, ld, _live(n_rows), _arg("h", h, g.dtype, g.shape),
-        *_kept("g_", rows, F, g_codes, g_scales), *_kept("u_", rows, F, u_codes, u_scales), _stream(stream)),
-        "moe_swiglu_keep8")
+        shape[0], shape[1], _ROW_TYPES[dt], pg, pu, ld, _opt("n_rows", n_rows, dev, torch.int32, (1,)),
+        _arg("h", h, dev, dt, shape), *_kept(dev, shape, g_codes, g_scales, "g_"),
+        *_kept(dev, shape, u_codes, u_scales, "u_"), _row_stream(stream, dev)), "moe_swiglu_keep8")
 
 
 def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=None, w_rows=None, dw=None,
@@ -391,23 +414,24 @@ def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=Non
     """The SwiGLU backward from the checkpoints of g and u: dg, du (one type, rows may be
     spaced alike), optionally h (the same type, dense) and dw = <dh, h> per row (at
     dw[row_slot[p]] when row_slot is given). w_rows scales dh per row in dg and du."""
-    pg, ld = _matrix("dg", dg)
-    pu, ldu = _matrix("du", du, dg.dtype, dg.shape)
-    rows, F = dg.shape
+    dev, f32 = _device(), torch.float32
+    pg, ld = _matrix("dg", dg, dev)
+    shape, dt = dg.shape, dg.dtype
+    pu, ldu = _matrix("du", du, dev, dt, shape)
     if ld != ldu:
         raise ValueError(f"dg and du: expected the same spacing of rows, got {ld} and {ldu}")
-    pd, ldd = _matrix("dh", dh, None, dg.shape)
-    if ldd != F:
+    pd, ldd = _matrix("dh", dh, dev, None, shape)
+    if ldd != shape[1]:
         raise ValueError("dh: expected a contiguous tensor")
-    f32 = torch.float32
-    if dw is not None and row_slot is None and dw.numel() != rows:
-        raise ValueError(f"dw: expected {rows} elements, got {dw.numel()}")
+    n_slots = 0 if dw is None else dw.numel()
+    if dw is not None and row_slot is None and n_slots != shape[0]:
+        raise ValueError(f"dw: expected {shape[0]} elements, got {n_slots}")
     _check(load_library().moe_swiglu_backward8(
-        rows, F, *_kept("g_", rows, F, g_codes, g_scales), *_kept("u_", rows, F, u_codes, u_scales), _live(n_rows),
-        _ROW_TYPES[dh.dtype], pd, _arg("w_rows", w_rows, f32, (rows,), True),
-        _arg("row_slot", row_slot, torch.int32, (rows,), True), 0 if dw is None else dw.numel(),
-        _ROW_TYPES[dg.dtype], pg, pu, ld, _arg("h", h, dg.dtype, dg.shape, True), _arg("dw", dw, f32, None, True),
-        _stream(stream)), "moe_swiglu_backward8")
+        shape[0], shape[1], *_kept(dev, shape, g_codes, g_scales, "g_"), *_kept(dev, shape, u_codes, u_scales, "u_"),
+        _opt("n_rows", n_rows, dev, torch.int32, (1,)), _ROW_TYPES[dh.dtype], pd,
+        _opt("w_rows", w_rows, dev, f32, (shape[0],)), _opt("row_slot", row_slot, dev, torch.int32, (shape[0],)),
+        n_slots, _ROW_TYPES[dt], pg, pu, ld, _opt("h", h, dev, dt, shape), _opt("dw", dw, dev, f32),
+        _row_stream(stream, dev)), "moe_swiglu_backward8")
 
 
 def moe_aux_stats(dims, logits, topk_idx, f, P, counts, scalars, ws, stream=None):
