@@ -98,7 +98,7 @@ typedef struct {
 /* Which workspace size moe_workspace_bytes() returns. */
 enum {
   MOE_WS_LAYER = 0, MOE_WS_ROUTE = 1, MOE_WS_PERMUTE = 2, MOE_WS_AUX = 3, MOE_WS_BACKWARD = 4,
-  MOE_WS_COMBINE_BACKWARD = 5
+  MOE_WS_COMBINE_BACKWARD = 5, MOE_WS_STATE8 = 6, MOE_WS_TRAIN8 = 7
 };
 
 typedef void* moe_stream; /* hipStream_t */
@@ -506,6 +506,32 @@ moe_status moe_layer_forward_train(const moe_dims* dims, const moe_layer_params*
 moe_status moe_layer_backward_saved(const moe_dims* dims, const moe_layer_params* params, const void* dy,
                                     float alpha, float beta, const moe_layer_grads* grads, void* ws,
                                     size_t ws_bytes, moe_stream stream);
+
+/*
+ * moe_layer_forward_train8 / moe_layer_backward_saved8 -- the training pair with what it
+ * keeps in 8 bits and apart from its workspace, so that a model's layers keep one state
+ * each and share one workspace. state: MOE_WS_STATE8 bytes, written by the forward and
+ * read by the backward: routing, permutation, pool counts and the 8-bit checkpoints
+ * (moe_act8_pack's format) of the pre-activations g and u, routed and shared: 2.06
+ * bytes per row and column instead of the 4 (g, u) and 2 (h) of the other pair. ws:
+ * MOE_WS_TRAIN8 bytes, scratch of each call, free in between (calls that overlap need
+ * their own).
+ * The forward computes y exactly as moe_layer_forward does (bit for bit); aux as in
+ * moe_layer_forward_train. The backward returns moe_layer_backward's gradients with g and
+ * u replaced by the values their checkpoints stand for, and h = silu(g) u of those, in
+ * the SwiGLU's derivative, dW_down and the routing weights' gradients; the selection,
+ * its weights and every other quantity are the forward's own. state must come from a
+ * forward_train8 call with the same dims, params and x (not checked). Limits as for
+ * moe_layer_backward (bf16, MOE_NULL_ZERO). Deterministic, no host synchronisation.
+ */
+moe_status moe_layer_forward_train8(const moe_dims* dims, const moe_layer_params* params, void* y,
+                                    const moe_aux_out* aux, void* state, size_t state_bytes, void* ws,
+                                    size_t ws_bytes, moe_stream stream);
+moe_status moe_layer_backward_saved8(const moe_dims* dims, const moe_layer_params* params,
+                                     const void* dy, float alpha, float beta,
+                                     const moe_layer_grads* grads, const void* state,
+                                     size_t state_bytes, void* ws, size_t ws_bytes,
+                                     moe_stream stream);
 
 /*
  * moe_validate_inputs -- optional check of the layer's inputs, not part of the

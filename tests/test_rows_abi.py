@@ -145,3 +145,42 @@ def test_binding_refuses_host_tensors():
         tcr.moe_act8_pack(x, f((4, 64), dtype=torch.int8), f((4, 2), dtype=torch.uint8))
     with pytest.raises(ValueError):
         tcr.moe_combine_rows(d, 9, rows, slots, w, None, x)
+
+
+def test_training_pair8_checks(lib):
+    """The 8-bit training pair refuses what moe_layer_backward does not cover, and bad
+    pointers, states and workspaces, before anything is launched."""
+    big = 1 << 40
+    p = tcr.LayerParams(FAKE, FAKE, 0.0, None, FAKE, FAKE, FAKE, None, None, None)
+    g = tcr.LayerGrads(FAKE, FAKE, FAKE, FAKE, FAKE, None, None, None)
+    d = _dims()
+    st, ws = tcr.workspace_bytes(d, tcr.MOE_WS_STATE8), tcr.workspace_bytes(d, tcr.MOE_WS_TRAIN8)
+    R, F = 64 * 2, 64
+    assert 2 * R * F * 33 // 32 <= st < tcr.workspace_bytes(d, tcr.MOE_WS_BACKWARD)
+    assert tcr.workspace_bytes(_dims(dtype=MOE_F32), tcr.MOE_WS_STATE8) == 0
+
+    def fwd(d, p=p, y=FAKE, aux=None, s=FAKE, sb=big, w=FAKE, wb=big):
+        return lib.moe_layer_forward_train8(ctypes.byref(d), ctypes.byref(p) if p else None, y,
+                                            ctypes.byref(aux) if aux else None, s, sb, w, wb, None)
+
+    def bwd(d, dy=FAKE, g=g, s=FAKE, sb=big, w=FAKE, wb=big):
+        return lib.moe_layer_backward_saved8(ctypes.byref(d), ctypes.byref(p), dy, 0.02, 0.001,
+                                             ctypes.byref(g) if g else None, s, sb, w, wb, None)
+
+    for call in (fwd, bwd):
+        assert call(_dims(dtype=MOE_F32)) == MOE_ERR_UNSUPPORTED
+        assert call(_dims(null_kind=tcr.MOE_NULL_COPY)) == MOE_ERR_UNSUPPORTED
+        assert call(d, sb=st - 1) == MOE_ERR_WORKSPACE
+        assert call(d, s=None) == MOE_ERR_WORKSPACE
+        assert call(d, s=MIS) == MOE_ERR_ALIGN
+        assert call(d, wb=ws - 1) == MOE_ERR_WORKSPACE
+        assert call(d, w=None) == MOE_ERR_WORKSPACE
+        assert call(_dims(T=0)) == MOE_OK
+    assert fwd(d, p=None) == MOE_ERR_ARG
+    assert fwd(d, y=None) == MOE_ERR_ARG
+    a = tcr.AuxOut()
+    a.logits = FAKE
+    assert fwd(d, aux=a) == MOE_ERR_ARG
+    assert bwd(d, g=None) == MOE_ERR_ARG
+    assert bwd(d, dy=None) == MOE_ERR_ARG
+    assert bwd(d, dy=MIS) == MOE_ERR_ALIGN

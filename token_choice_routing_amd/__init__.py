@@ -25,7 +25,7 @@ MOE_F32, MOE_BF16, MOE_F16 = 0, 1, 2
 MOE_NULL_ZERO, MOE_NULL_COPY, MOE_NULL_CONSTANT = 0, 1, 2
 NULL_KINDS = {"zero": MOE_NULL_ZERO, "copy": MOE_NULL_COPY, "constant": MOE_NULL_CONSTANT}
 (MOE_WS_LAYER, MOE_WS_ROUTE, MOE_WS_PERMUTE, MOE_WS_AUX, MOE_WS_BACKWARD,
- MOE_WS_COMBINE_BACKWARD) = range(6)
+ MOE_WS_COMBINE_BACKWARD, MOE_WS_STATE8, MOE_WS_TRAIN8) = range(8)
 MOE_GEMM_GATE_UP, MOE_GEMM_DOWN = 0, 1
 
 
@@ -96,6 +96,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
                                     ctypes.c_size_t, _P],
         "moe_layer_backward_saved": [D, ctypes.POINTER(LayerParams), _P, ctypes.c_float, ctypes.c_float,
                                      ctypes.POINTER(LayerGrads), _P, ctypes.c_size_t, _P],
+        "moe_layer_forward_train8": [D, ctypes.POINTER(LayerParams), _P, ctypes.POINTER(AuxOut), _P,
+                                     ctypes.c_size_t, _P, ctypes.c_size_t, _P],
+        "moe_layer_backward_saved8": [D, ctypes.POINTER(LayerParams), _P, ctypes.c_float, ctypes.c_float,
+                                      ctypes.POINTER(LayerGrads), _P, ctypes.c_size_t, _P, ctypes.c_size_t, _P],
         "moe_validate_inputs": [D, ctypes.POINTER(LayerParams), _P, ctypes.c_size_t, _P],
     }
     for name, args in sig.items():
@@ -482,6 +486,24 @@ def moe_layer_backward_saved(dims, params: LayerParams, dy, alpha: float, beta: 
     _check(load_library().moe_layer_backward_saved(ctypes.byref(dims), ctypes.byref(params), _ptr(dy),
                                                     float(alpha), float(beta), ctypes.byref(grads), wp, wb,
                                                     _stream(stream)), "moe_layer_backward_saved")
+
+
+def moe_layer_forward_train8(dims, params: LayerParams, y, aux: AuxOut = None, state=None, ws=None, stream=None):
+    """The training forward that keeps its state in 8 bits in state (MOE_WS_STATE8 bytes)
+    for moe_layer_backward_saved8; ws (MOE_WS_TRAIN8 bytes) is scratch of the call."""
+    (sp, sb), (wp, wb) = _ws(state), _ws(ws)
+    _check(load_library().moe_layer_forward_train8(ctypes.byref(dims), ctypes.byref(params), _ptr(y),
+                                                    ctypes.byref(aux) if aux is not None else None, sp, sb, wp, wb,
+                                                    _stream(stream)), "moe_layer_forward_train8")
+
+
+def moe_layer_backward_saved8(dims, params: LayerParams, dy, alpha: float, beta: float, grads: LayerGrads,
+                              state=None, ws=None, stream=None):
+    """moe_layer_backward from the 8-bit state a moe_layer_forward_train8 call left in state."""
+    (sp, sb), (wp, wb) = _ws(state), _ws(ws)
+    _check(load_library().moe_layer_backward_saved8(ctypes.byref(dims), ctypes.byref(params), _ptr(dy),
+                                                     float(alpha), float(beta), ctypes.byref(grads), sp, sb, wp, wb,
+                                                     _stream(stream)), "moe_layer_backward_saved8")
 
 
 def moe_validate_inputs(dims, params: LayerParams, ws, stream=None) -> bool:

@@ -19,6 +19,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "act8.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 #include "rows.hpp"
@@ -41,26 +42,16 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
 }
 
-// The quad's scale byte for eight values per lane (lanes past the row hold zeros). As
-// integers, magnitudes order like the floats, with NaN above infinity.
+// The quad's scale byte for eight values per lane (lanes past the row hold zeros).
 __device__ __forceinline__ uint32_t block_scale(const float* v) {
   uint32_t m = 0;
 #pragma unroll
-  for (int j = 0; j < kCols; ++j) m = max(m, __float_as_uint(v[j]) & 0x7fffffffu);
-  m = quad_max(m) >> 23;  // biased exponent of amax: floor(log2 amax) + 127 (0: below 2^-126)
-  return m == 255 ? 255 : (uint32_t)max((int)m - 6, 1);
+  for (int j = 0; j < kCols; ++j) m = max(m, act8_magnitude(v[j]));
+  return act8_scale(quad_max(m));
 }
 
-// Eight codes: v 2^-e + 1.5 2^23 rounds to an integer (nearest even) in the low bits.
 __device__ __forceinline__ u32x2_t encode(const float* v, uint32_t scale) {
-  if (scale == 255) return u32x2_t{0, 0};
-  const float inv = __uint_as_float((254 - scale) << 23);  // 2^-e
-  constexpr float kMagic = 12582912.0f;
-  uint32_t q[kCols];
-#pragma unroll
-  for (int j = 0; j < kCols; ++j)
-    q[j] = __float_as_uint(fminf(fmaxf(fmaf(v[j], inv, kMagic), kMagic - 127.0f), kMagic + 127.0f)) & 0xff;
-  return u32x2_t{q[0] | (q[1] << 8) | (q[2] << 16) | (q[3] << 24), q[4] | (q[5] << 8) | (q[6] << 16) | (q[7] << 24)};
+  return u32x2_t{act8_encode(v[0], v[1], v[2], v[3], scale), act8_encode(v[4], v[5], v[6], v[7], scale)};
 }
 
 // Eight values q 2^e, exact (0 times the NaN block's infinite scale is NaN).

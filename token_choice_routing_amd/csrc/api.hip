@@ -249,8 +249,13 @@ static bool wgrad_kmajor_ok(const moe_dims* d) {
   return gemm_kmajor_ok(k.wd, k.wsd) && gemm_kmajor_ok(k.wg, k.wu) && gemm_kmajor_ok(k.wsg, k.wsu);
 }
 
-BwdWs bwd_ws(const moe_dims* d) {
+bool keep_preacts(const moe_dims* d);
+
+// eight: the pair whose state is kept in 8 bits apart from the workspace; g and u are
+// then written in it only where the gate/up launch cannot encode them itself.
+BwdWs bwd_ws(const moe_dims* d, bool eight = false) {
   BwdWs w{};
+  const bool no_gu = eight && keep_preacts(d);
   w.km = dgrad_kmajor_ok(d);
   w.km2 = wgrad_kmajor_ok(d);
   w.fwd = layer_ws(d);
@@ -265,8 +270,8 @@ BwdWs bwd_ws(const moe_dims* d) {
     return at;
   };
   w.f = take((size_t)(N + M) * 4);
-  w.g = take((size_t)R * F * 4);
-  w.u = take((size_t)R * F * 4);
+  w.g = no_gu ? 0 : take((size_t)R * F * 4);
+  w.u = no_gu ? 0 : take((size_t)R * F * 4);
   w.h = take((size_t)R * F * 2);
   w.dyp = take((size_t)R * dm * 2);
   w.wperm = take((size_t)R * 4);
@@ -286,8 +291,8 @@ BwdWs bwd_ws(const moe_dims* d) {
   w.xp = w.km2 ? take((size_t)R * dm * 2) : 0;
   w.rpart = take(router_wgrad_ws_bytes(T, N + 1, (int)dm));
   if (Fs) {
-    w.gs = take((size_t)T * Fs * 4);
-    w.us = take((size_t)T * Fs * 4);
+    w.gs = no_gu ? 0 : take((size_t)T * Fs * 4);
+    w.us = no_gu ? 0 : take((size_t)T * Fs * 4);
     w.hs = take((size_t)T * Fs * 2);
     w.dhs = take((size_t)T * Fs * 4);
     w.dgus = take((size_t)T * 2 * Fs * 2);
@@ -306,6 +311,63 @@ BwdWs bwd_ws(const moe_dims* d) {
   }
   w.total = o;
   return w;
+}
+
+// What the layer's backward reads of its forward: routing, permutation, pool counts and,
+// with eight set, the 8-bit checkpoints of the expert pre-activations (else those stay
+// in the backward workspace).
+struct BwdState {
+  bool eight;
+  float* logits;
+  int32_t* topk_idx;
+  float* topk_w;
+  int32_t *offsets, *perm_token, *slot_pos;
+  float* f;
+  uint8_t *cg, *sg, *cu, *su;      // routed codes and scale bytes
+  uint8_t *cgs, *sgs, *cus, *sus;  // shared
+};
+
+BwdState ws_state(const BwdWs& W, uint8_t* base) {
+  const LayerWs& L = W.fwd;
+  auto fp = [&](size_t off) { return reinterpret_cast<float*>(base + off); };
+  auto ip = [&](size_t off) { return reinterpret_cast<int32_t*>(base + off); };
+  return BwdState{false, fp(L.logits), ip(L.topk_idx), fp(L.topk_w), ip(L.offsets), ip(L.perm_token),
+                  ip(L.slot_pos), fp(W.f)};
+}
+
+// The state buffer of the 8-bit pair: its size, and its pieces at base.
+size_t state8(const moe_dims* d, uint8_t* base, BwdState& st) {
+  const int64_t T = d->T, TK = T * d->top_k, R = max_rows(d), F = d->d_ff, Fs = d->d_ff_shared;
+  const int N = d->n_experts, M = d->n_null;
+  size_t o = 0;
+  auto take = [&](size_t bytes) {
+    uint8_t* at = base ? base + o : nullptr;
+    o += align_up(bytes);
+    return at;
+  };
+  auto fp = [&](size_t n) { return reinterpret_cast<float*>(take(n * 4)); };
+  auto ip = [&](size_t n) { return reinterpret_cast<int32_t*>(take(n * 4)); };
+  st.eight = true;
+  st.logits = fp((size_t)T * (N + 1));
+  st.topk_idx = ip(TK);
+  st.topk_w = fp(TK);
+  st.offsets = ip(N + 1);
+  st.perm_token = ip(R);
+  st.slot_pos = ip(TK);
+  st.f = fp(N + M);
+  st.cg = take((size_t)R * F);
+  st.sg = take((size_t)R * ((F + 31) / 32));
+  st.cu = take((size_t)R * F);
+  st.su = take((size_t)R * ((F + 31) / 32));
+  st.cgs = take((size_t)T * Fs);
+  st.sgs = take((size_t)T * ((Fs + 31) / 32));
+  st.cus = take((size_t)T * Fs);
+  st.sus = take((size_t)T * ((Fs + 31) / 32));
+  return o;
+}
+size_t state8_bytes(const moe_dims* d) {
+  BwdState st;
+  return state8(d, nullptr, st);
 }
 
 }  // namespace
@@ -364,6 +426,8 @@ size_t moe_workspace_bytes(const moe_dims* d, int32_t which) {
     case MOE_WS_PERMUTE: return permute_ws_bytes(d->T, d->n_experts);
     case MOE_WS_AUX: return aux_ws_bytes(d->n_experts, d->n_null);
     case MOE_WS_BACKWARD: return d->dtype == MOE_BF16 ? bwd_ws(d).total : 0;
+    case MOE_WS_STATE8: return d->dtype == MOE_BF16 ? state8_bytes(d) : 0;
+    case MOE_WS_TRAIN8: return d->dtype == MOE_BF16 ? bwd_ws(d, true).total : 0;
     case MOE_WS_COMBINE_BACKWARD: return combine_bwd_ws_bytes(d->T, d->d_model, d->null_kind);
   }
   return 0;
@@ -936,10 +1000,17 @@ static moe_status check_backward_args(const moe_dims* d, const moe_layer_params*
   return MOE_OK;
 }
 
+// The 8-bit pair's state buffer.
+static moe_status check_state8(const moe_dims* d, const void* state, size_t bytes) {
+  if (!state || bytes < state8_bytes(d)) return MOE_ERR_WORKSPACE;
+  return need(state);
+}
+
 // Whether the expert pre-activations come from the keep-mode launch (g and u stored in
 // IEEE half) rather than plain GEMMs (float32): the 256 x 256 tiles take the routed and
 // the shared gate/up problems (a function of the dims).
-static bool keep_preacts(const moe_dims* d) {
+namespace {
+bool keep_preacts(const moe_dims* d) {
   static const int32_t one = 1;  // a non-null row index and offsets pointer for the shape test
   GemmProblem r{}, sh{};
   r.a_rows = &one;
@@ -957,15 +1028,17 @@ static bool keep_preacts(const moe_dims* d) {
   }
   return gemm_pair_uses_pp(r, sh);
 }
+}  // namespace
 
-// The layer state the backward works from, written into the backward workspace:
+// The layer state the backward works from, written into the backward workspace (or, for
+// the 8-bit pair, into its state buffer st):
 // routing (logits, selection, weights), the permutation, the pool counts f, and the
 // expert pre-activations g, u (float32) and h (bf16), routed and shared. With fwd set
 // (the training forward) also the half-precision h and hs of the layer forward's
 // layout, the row redirect of the fused combine, and the caller's statistics outputs
 // (P, counts, scalars).
 static moe_status backward_state(const moe_dims* d, const moe_layer_params* p, const BwdWs& W, uint8_t* base,
-                                 hipStream_t s, const moe_aux_out* fwd) {
+                                 hipStream_t s, const moe_aux_out* fwd, const BwdState& st) {
   auto at = [&](size_t off) { return static_cast<void*>(base + off); };
   auto fp = [&](size_t off) { return static_cast<float*>(at(off)); };
   auto ip = [&](size_t off) { return static_cast<int32_t*>(at(off)); };
@@ -975,19 +1048,19 @@ static moe_status backward_state(const moe_dims* d, const moe_layer_params* p, c
   const int N = d->n_experts, M = d->n_null, K = d->top_k;
   const int cus = cu_count();
   const uint16_t* x16 = static_cast<const uint16_t*>(p->x);
-  int32_t* offsets = ip(L.offsets);
-  int32_t* perm_token = ip(L.perm_token);
+  int32_t* offsets = st.offsets;
+  int32_t* perm_token = st.perm_token;
   int32_t* permute_ws = ip(L.permute);
   // 1-2. routing, permutation and pool counts f
   RouteArgs ra{T, d->d_model, N, M, K, true, true, p->x, p->w_router, p->null_bias, p->null_bias_tok,
-               nullptr, fp(L.logits), ip(L.topk_idx), fp(L.topk_w), ip(L.n_real), at(L.route), permute_ws,
+               nullptr, st.logits, st.topk_idx, st.topk_w, ip(L.n_real), at(L.route), permute_ws,
                ip(L.rhist), static_cast<double*>(at(L.tstats)), d->null_kind};
   HIP_TRY(launch_route(ra, s));
-  AuxTiles af{static_cast<double*>(at(L.tstats)), ip(L.rhist), fp(W.f), fwd ? fwd->P : nullptr,
+  AuxTiles af{static_cast<double*>(at(L.tstats)), ip(L.rhist), st.f, fwd ? fwd->P : nullptr,
               fwd ? fwd->counts : nullptr, fwd ? fwd->scalars : nullptr};
   int32_t* row_dst = fwd && fused_combine(d) ? ip(L.row_dst) : nullptr;
-  PermuteArgs pa{T, K, N, M, d->d_model, 2, ip(L.topk_idx), nullptr, ip(L.counts), offsets, perm_token,
-                 ip(L.slot_pos), nullptr, permute_ws, true, &af, row_dst};
+  PermuteArgs pa{T, K, N, M, d->d_model, 2, st.topk_idx, nullptr, ip(L.counts), offsets, perm_token,
+                 st.slot_pos, nullptr, permute_ws, true, &af, row_dst};
   HIP_TRY(launch_permute(pa, s));
   // 3. expert pre-activations g = x W_g^T, u = x W_u^T (float32) and h = silu(g) u (bf16):
   // routed and shared in one launch whose epilogue keeps g and u and writes h, when the
@@ -1005,6 +1078,48 @@ static moe_status backward_state(const moe_dims* d, const moe_layer_params* p, c
   }
   // (the same test as gemm_pair_uses_pp(gk, gsk); the gradient step reads g and u by it)
   const bool keep = keep_preacts(d);
+  if (st.eight) {
+    if (keep) {
+      // the layer forward's gate/up launch, whose epilogue also encodes g and u
+      gk.out = at(L.h);
+      gk.keep_g = st.cg;
+      gk.keep_u = st.cu;
+      gk.keep_sg = st.sg;
+      gk.keep_su = st.su;
+      if (Fs) {
+        gsk.out = at(L.hs);
+        gsk.keep_g = st.cgs;
+        gsk.keep_u = st.cus;
+        gsk.keep_sg = st.sgs;
+        gsk.keep_su = st.sus;
+      }
+      HIP_TRY(launch_gemm_pair(true, 5, gk, gsk, cus, s, 2));
+      return MOE_OK;
+    }
+    HIP_TRY(launch_layer_gate_up(d, p->x, perm_token, offsets, p->w_gate, p->w_up, p->ws_gate, p->ws_up, at(L.h),
+                                 at(L.hs), s));
+    gk.b1 = nullptr;
+    gk.out = at(W.g);
+    gk.keep_g = gk.keep_u = nullptr;
+    GemmProblem uk = gk;
+    uk.b0 = static_cast<const uint16_t*>(p->w_up);
+    uk.out = at(W.u);
+    HIP_TRY(launch_gemm_pair(true, 1, gk, uk, cus, s, 3));
+    HIP_TRY(launch_act8_pack(MOE_F32, at(W.g), F, offsets + N, R, (int)F, st.cg, st.sg, s));
+    HIP_TRY(launch_act8_pack(MOE_F32, at(W.u), F, offsets + N, R, (int)F, st.cu, st.su, s));
+    if (Fs) {
+      gsk.b1 = nullptr;
+      gsk.out = at(W.gs);
+      gsk.keep_g = gsk.keep_u = nullptr;
+      GemmProblem usk = gsk;
+      usk.b0 = static_cast<const uint16_t*>(p->ws_up);
+      usk.out = at(W.us);
+      HIP_TRY(launch_gemm_pair(true, 1, gsk, usk, cus, s, 3));
+      HIP_TRY(launch_act8_pack(MOE_F32, at(W.gs), Fs, nullptr, T, (int)Fs, st.cgs, st.sgs, s));
+      HIP_TRY(launch_act8_pack(MOE_F32, at(W.us), Fs, nullptr, T, (int)Fs, st.cus, st.sus, s));
+    }
+    return MOE_OK;
+  }
   if (keep && fwd) {
     // the forward's half-precision h (and hs) from the same epilogue: bit for bit what the
     // layer forward's gate/up launch writes
@@ -1034,15 +1149,17 @@ static moe_status backward_state(const moe_dims* d, const moe_layer_params* p, c
   return MOE_OK;
 }
 
-// The backward from the state in the workspace: recomputed first (recompute), or left
-// there by moe_layer_forward_train.
+// The backward from the state in the workspace, recomputed first (recompute) or left
+// there by moe_layer_forward_train, or from the 8-bit pair's state buffer (kept, with
+// eight set).
 static moe_status layer_backward(const moe_dims* d, const moe_layer_params* p, const void* dy, float alpha,
                                  float beta, const moe_layer_grads* gr, void* ws, size_t ws_bytes, moe_stream stream,
-                                 bool recompute) {
+                                 bool recompute, bool eight = false, void* kept = nullptr, size_t kept_bytes = 0) {
   MOE_TRY(check_dims(d));
   if (!p || !gr) return MOE_ERR_ARG;
-  const BwdWs W = bwd_ws(d);
+  const BwdWs W = bwd_ws(d, eight);
   MOE_TRY(check_backward_args(d, p, W, ws, ws_bytes));
+  if (eight) MOE_TRY(check_state8(d, kept, kept_bytes));
   const int64_t T = d->T, dm = d->d_model, F = d->d_ff, Fs = d->d_ff_shared;
   if (Fs) {
     MOE_TRY(need(gr->dws_gate));
@@ -1061,13 +1178,14 @@ static moe_status layer_backward(const moe_dims* d, const moe_layer_params* p, c
   auto at = [&](size_t off) { return static_cast<void*>(base + off); };
   auto fp = [&](size_t off) { return static_cast<float*>(at(off)); };
   auto ip = [&](size_t off) { return static_cast<int32_t*>(at(off)); };
-  const LayerWs& L = W.fwd;
-  float* logits = fp(L.logits);
-  int32_t* topk_idx = ip(L.topk_idx);
-  float* topk_w = fp(L.topk_w);
-  int32_t* offsets = ip(L.offsets);
-  int32_t* perm_token = ip(L.perm_token);
-  int32_t* slot_pos = ip(L.slot_pos);
+  BwdState st = ws_state(W, base);
+  if (eight) state8(d, static_cast<uint8_t*>(kept), st);
+  float* logits = st.logits;
+  int32_t* topk_idx = st.topk_idx;
+  float* topk_w = st.topk_w;
+  int32_t* offsets = st.offsets;
+  int32_t* perm_token = st.perm_token;
+  int32_t* slot_pos = st.slot_pos;
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t R = max_rows(d);
   const int N = d->n_experts, M = d->n_null, K = d->top_k;
@@ -1076,7 +1194,7 @@ static moe_status layer_backward(const moe_dims* d, const moe_layer_params* p, c
   MOE_TRY(no_pending_error());
 
   // 1-3. routing, permutation, pool counts and expert pre-activations
-  if (recompute) MOE_TRY(backward_state(d, p, W, base, s, nullptr));
+  if (recompute) MOE_TRY(backward_state(d, p, W, base, s, nullptr, st));
 
   // 4. per real slot: its expert row's dY = g dy (bf16, for dW_down), g and slot index
   HIP_TRY(launch_slot_rows(dy, slot_pos, topk_w, T, K, (int)dm, R, at(W.dyp), fp(W.wperm), ip(W.rslot), fp(W.dw),
@@ -1112,11 +1230,26 @@ static moe_status layer_backward(const moe_dims* d, const moe_layer_params* p, c
     hs3 = km.hs3;
   }
   HIP_TRY(launch_gemm_pair(true, 1, h3, hs3, cus, s, 3));
-  const bool g16 = keep_preacts(d);
-  HIP_TRY(launch_swiglu_bwd_routed(at(W.g), at(W.u), g16, fp(W.dh), at(W.h), fp(W.wperm), ip(W.rslot), offsets, N, R,
-                                    (int)F, at(W.dgu), fp(W.dw), s));
-  if (Fs) HIP_TRY(launch_swiglu_bwd(at(W.gs), at(W.us), g16, fp(W.dhs), nullptr, 1, T, (int)Fs, at(W.dgus), s));
-  HIP_TRY(launch_router_bwd(logits, topk_idx, topk_w, fp(W.dw), fp(W.f), T, N, M, K, alpha, beta, fp(W.ds), s));
+  if (eight) {
+    // the same from the 8-bit checkpoints, which also give h back for the down
+    // projections' weight gradients
+    const SwigluBwd8Args routed{R, (int)F, st.cg, st.sg, st.cu, st.su, offsets + N, MOE_F32, at(W.dh), fp(W.wperm),
+                                ip(W.rslot), T * K, MOE_BF16, at(W.dgu), static_cast<uint16_t*>(at(W.dgu)) + F, 2 * F,
+                                at(W.h), fp(W.dw)};
+    HIP_TRY(launch_swiglu_bwd8(routed, s));
+    if (Fs) {
+      const SwigluBwd8Args shared{T, (int)Fs, st.cgs, st.sgs, st.cus, st.sus, nullptr, MOE_F32, at(W.dhs), nullptr,
+                                  nullptr, 0, MOE_BF16, at(W.dgus), static_cast<uint16_t*>(at(W.dgus)) + Fs, 2 * Fs,
+                                  at(W.hs), nullptr};
+      HIP_TRY(launch_swiglu_bwd8(shared, s));
+    }
+  } else {
+    const bool g16 = keep_preacts(d);
+    HIP_TRY(launch_swiglu_bwd_routed(at(W.g), at(W.u), g16, fp(W.dh), at(W.h), fp(W.wperm), ip(W.rslot), offsets, N, R,
+                                      (int)F, at(W.dgu), fp(W.dw), s));
+    if (Fs) HIP_TRY(launch_swiglu_bwd(at(W.gs), at(W.us), g16, fp(W.dhs), nullptr, 1, T, (int)Fs, at(W.dgus), s));
+  }
+  HIP_TRY(launch_router_bwd(logits, topk_idx, topk_w, fp(W.dw), st.f, T, N, M, K, alpha, beta, fp(W.ds), s));
 
   // 7. da = [dg | du] [W_g ; W_u]: routed rows and shared rows (float32)
   GemmProblem a4{bf(W.dgu), nullptr, R, offsets, N, R, bf(W.wguT), nullptr, (int)dm, (int)(2 * F), at(W.dxp)};
@@ -1210,16 +1343,20 @@ moe_status moe_layer_backward_saved(const moe_dims* d, const moe_layer_params* p
   return layer_backward(d, p, dy, alpha, beta, gr, ws, ws_bytes, stream, false);
 }
 
-moe_status moe_layer_forward_train(const moe_dims* d, const moe_layer_params* p, void* y, const moe_aux_out* aux,
-                                   void* ws, size_t ws_bytes, moe_stream stream) {
+// The training forward: the state for the backward (in the workspace, or in the 8-bit
+// pair's state buffer), then the layer's down projections and combine.
+static moe_status layer_forward_train(const moe_dims* d, const moe_layer_params* p, void* y, const moe_aux_out* aux,
+                                      bool eight, void* kept, size_t kept_bytes, void* ws, size_t ws_bytes,
+                                      moe_stream stream) {
   MOE_TRY(check_dims(d));
   if (!p) return MOE_ERR_ARG;
-  const BwdWs W = bwd_ws(d);
+  const BwdWs W = bwd_ws(d, eight);
   MOE_TRY(check_backward_args(d, p, W, ws, ws_bytes));
+  if (eight) MOE_TRY(check_state8(d, kept, kept_bytes));
   MOE_TRY(need(y));
   moe_aux_out ao{};
   if (aux) ao = *aux;
-  // the routing outputs and f stay in the workspace (the backward reads them there)
+  // the routing outputs and f stay in the state (the backward reads them there)
   if (ao.logits || ao.topk_idx || ao.topk_w || ao.n_real || ao.offsets || ao.f) return MOE_ERR_ARG;
   MOE_TRY(maybe(ao.P));
   MOE_TRY(maybe(ao.counts));
@@ -1227,14 +1364,32 @@ moe_status moe_layer_forward_train(const moe_dims* d, const moe_layer_params* p,
   if (d->T == 0) return MOE_OK;
   MOE_TRY(no_pending_error());
   uint8_t* base = static_cast<uint8_t*>(ws);
+  BwdState st = ws_state(W, base);
+  if (eight) state8(d, static_cast<uint8_t*>(kept), st);
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  MOE_TRY(backward_state(d, p, W, base, s, &ao));
+  MOE_TRY(backward_state(d, p, W, base, s, &ao, st));
   const LayerWs& L = W.fwd;
   auto at = [&](size_t off) { return static_cast<void*>(base + off); };
-  return layer_down_combine(d, p, y, L, base, static_cast<const int32_t*>(at(L.offsets)),
-                            static_cast<const int32_t*>(at(L.slot_pos)), static_cast<const float*>(at(L.topk_w)),
+  return layer_down_combine(d, p, y, L, base, st.offsets, st.slot_pos, st.topk_w,
                             static_cast<const int32_t*>(at(L.n_real)),
                             fused_combine(d) ? static_cast<const int32_t*>(at(L.row_dst)) : nullptr, s);
+}
+
+moe_status moe_layer_forward_train(const moe_dims* d, const moe_layer_params* p, void* y, const moe_aux_out* aux,
+                                   void* ws, size_t ws_bytes, moe_stream stream) {
+  return layer_forward_train(d, p, y, aux, false, nullptr, 0, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_forward_train8(const moe_dims* d, const moe_layer_params* p, void* y, const moe_aux_out* aux,
+                                    void* state, size_t state_bytes, void* ws, size_t ws_bytes, moe_stream stream) {
+  return layer_forward_train(d, p, y, aux, true, state, state_bytes, ws, ws_bytes, stream);
+}
+
+moe_status moe_layer_backward_saved8(const moe_dims* d, const moe_layer_params* p, const void* dy, float alpha,
+                                     float beta, const moe_layer_grads* gr, const void* state, size_t state_bytes,
+                                     void* ws, size_t ws_bytes, moe_stream stream) {
+  return layer_backward(d, p, dy, alpha, beta, gr, ws, ws_bytes, stream, false, true, const_cast<void*>(state),
+                        state_bytes);
 }
 
 }  // extern "C"

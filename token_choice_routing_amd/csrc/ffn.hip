@@ -47,6 +47,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "act8.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 
@@ -75,7 +76,9 @@ constexpr int kMaxGroups = 512;
 // kSwiGLUKeep: kSwiGLU for the backward's recompute (256 x 256 tiles only): the epilogue
 //          stores g and u (IEEE half, keep_g / keep_u) and h = silu(g) u as bf16 (from the
 //          float32 g and u).
-enum { kSwiGLU = 0, kPlain = 1, kDown16 = 2, kDownComb = 3, kPlainKM = 4, kPlainKM2 = 5, kSwiGLUKeep = 6 };
+// kSwiGLUKeep8: kSwiGLU that also stores the 8-bit checkpoints of the float32 g and u
+//          (keep_g / keep_u codes, keep_sg / keep_su scale bytes; 256 x 256 tiles only).
+enum { kSwiGLU = 0, kPlain = 1, kDown16 = 2, kDownComb = 3, kPlainKM = 4, kPlainKM2 = 5, kSwiGLUKeep = 6, kSwiGLUKeep8 = 7 };
 
 // One 32x32x16 MFMA step: the weight fragment w (bf16 bits) and the activation
 // fragment a (bf16 bits, or half bits for kDown16).
@@ -782,6 +785,65 @@ __device__ __forceinline__ void combine_epilogue(const GemmProblem& pr, int m0, 
   }
 }
 
+// The gate/up epilogue that keeps its pre-activations in 8 bits (kSwiGLUKeep8). The
+// wavefront holds rows rbase + 32 g + l32 and in each row 32 columns from c0, one block of
+// the checkpoint: lane half h has columns 8 q + 4 h + j, so a block's largest magnitude is
+// that of two lanes, 32 apart. Their code words change places pairwise (q 0 with q 2, q 1
+// with q 3), after which each lane holds 16 neighbouring columns and stores them at once.
+__device__ __forceinline__ void keep8_epilogue(const GemmProblem& pr, int m0, int rows_valid, int rbase, int c0,
+                                               f32x16_t (&acc)[2][4]) {
+  const int lane = opaque_v((int)threadIdx.x) & (kWave - 1), half = lane >> 5, l32 = lane & 31;
+  const int Nout = pr.n_out;
+  const int64_t nb = (Nout + 31) / 32;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    const int rl = rbase + g * 32 + l32;
+    const bool on = rl < rows_valid;
+    const int64_t row = m0 + (on ? rl : 0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const f32x16_t& v = acc[s][g];
+      uint32_t amax = 0;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) amax = max(amax, act8_magnitude(v[j]));
+      amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32, kWave));
+      const uint32_t scale = act8_scale(amax);
+      uint32_t q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = act8_encode(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], scale);
+      u32x4_t w;  // columns 16 half .. 16 half + 15 of the block
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t other = (uint32_t)__shfl_xor((int)(half ? q[i] : q[i + 2]), 32, kWave);
+        w[2 * i] = half ? other : q[i];
+        w[2 * i + 1] = half ? q[i + 2] : other;
+      }
+      uint8_t* codes = static_cast<uint8_t*>(s ? pr.keep_u : pr.keep_g) + row * Nout;
+      const int col = c0 + 16 * half;
+      if (on && (Nout & 15) == 0) {
+        if (col < Nout) *reinterpret_cast<u32x4_t*>(codes + col) = w;
+      } else if (on) {  // rows that start at multiples of 8 only
+        if (col < Nout) *reinterpret_cast<u32x2_t*>(codes + col) = u32x2_t{w[0], w[1]};
+        if (col + 8 < Nout) *reinterpret_cast<u32x2_t*>(codes + col + 8) = u32x2_t{w[2], w[3]};
+      }
+      if (on && half == s && c0 < Nout)
+        static_cast<uint8_t*>(s ? pr.keep_su : pr.keep_sg)[row * nb + c0 / 32] = (uint8_t)scale;
+    }
+    if (!on) continue;
+    bf16_t* crow = static_cast<bf16_t*>(pr.out) + row * Nout;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int col = c0 + 8 * q + 4 * half;
+      if (col < Nout) {
+        float h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[j] = silu(acc[0][g][4 * q + j]) * acc[1][g][4 * q + j];
+        *reinterpret_cast<u32x2_t*>(crow + col) = u32x2_t{pack_f16x2(h[0], h[1]), pack_f16x2(h[2], h[3])};
+      }
+    }
+  }
+}
+
 constexpr size_t kPpLds = (size_t)kPpS * (kPpBM + kPpBN) * kPpBK * sizeof(bf16_t);  // 128 KB
 
 // SIMD of the calling wavefront within its CU (HW_ID bits 5:4).
@@ -800,7 +862,7 @@ template <int MODE, int ROLE>
 __global__ void __launch_bounds__(64 * kPpNW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 grouped_gemm_pp_kernel(GemmProblem p0, GemmProblem p1) {
   constexpr int BM = kPpBM, BN = kPpBN, BK = kPpBK, S = kPpS, NW = kPpNW;
-  constexpr bool SW = MODE == kSwiGLU || MODE == kSwiGLUKeep;  // gate and up weight halves
+  constexpr bool SW = MODE == kSwiGLU || MODE == kSwiGLUKeep || MODE == kSwiGLUKeep8;  // gate and up weight halves
   constexpr int OC = SW ? BN / 2 : BN;  // output columns per tile
   constexpr int FM = 4, FN = 2;                      // 32-row blocks per wavefront: activations, weights
   constexpr bool KM = MODE == kPlainKM || MODE == kPlainKM2;  // K-major weights
@@ -1206,6 +1268,8 @@ grouped_gemm_pp_kernel(GemmProblem p0, GemmProblem p1) {
     }
     if constexpr (MODE == kDownComb) {
       if (wact) combine_epilogue(cur.second ? p1 : p0, cur.m0, cur.rows_valid, wm * (BM / 2), cur.col0 + wn * 64, acc);
+    } else if constexpr (MODE == kSwiGLUKeep8) {
+      if (wact) keep8_epilogue(cur.second ? p1 : p0, cur.m0, cur.rows_valid, wm * (BM / 2), cur.col0 + wn * 32, acc);
     } else if (wact) {
       const GemmProblem pr = cur.second ? p1 : p0;
       const int Nout = pr.n_out, m0 = cur.m0, rows_valid = cur.rows_valid, col0 = cur.col0;
@@ -1579,9 +1643,12 @@ hipError_t launch_gemm_pair(bool bf16, int op, const GemmProblem& p0, const Gemm
   // the output-row redirect (the layer's down projection launch) and the combine
   // epilogue exist on the 256 x 256 tiles only
   const bool redirect = (any0 && p0.out_rows) || (any1 && p1.out_rows);
-  if ((op == 3 || op == 4 || redirect) && (!bf16 || !gemm_pair_uses_pp(p0, p1))) return hipErrorInvalidValue;
+  if ((op == 3 || op == 4 || op == 5 || redirect) && (!bf16 || !gemm_pair_uses_pp(p0, p1))) return hipErrorInvalidValue;
   if (op == 4 && ((any0 && (!p0.keep_g || !p0.keep_u || p0.n_out % 4)) || (any1 && (!p1.keep_g || !p1.keep_u ||
                                                                                    p1.n_out % 4))))
+    return hipErrorInvalidValue;
+  if (op == 5 && ((any0 && (!p0.keep_g || !p0.keep_u || !p0.keep_sg || !p0.keep_su || p0.n_out % 8)) ||
+                  (any1 && (!p1.keep_g || !p1.keep_u || !p1.keep_sg || !p1.keep_su || p1.n_out % 8))))
     return hipErrorInvalidValue;
   if (redirect && (op != 2 || role != 2)) return hipErrorInvalidValue;
   const bool km = (any0 && p0.b_kmajor) || (any1 && p1.b_kmajor);
@@ -1606,6 +1673,11 @@ hipError_t launch_gemm_pair(bool bf16, int op, const GemmProblem& p0, const Gemm
     if (op == 4) {
       if (role == 3) launch_pp<kSwiGLUKeep, 3>(q0, q1, num_cus, stream);
       else if (role == 2) launch_pp<kSwiGLUKeep, 2>(q0, q1, num_cus, stream);
+      else return hipErrorInvalidValue;
+      return hipGetLastError();
+    }
+    if (op == 5) {
+      if (role == 2) launch_pp<kSwiGLUKeep8, 2>(q0, q1, num_cus, stream);
       else return hipErrorInvalidValue;
       return hipGetLastError();
     }

@@ -147,14 +147,19 @@ struct GemmProblem {
   // op 4, optional: h also stored as IEEE half here (the forward's down-projection input,
   // bit for bit what op 0 writes), for a forward that keeps its pre-activations
   void* keep_h16;
+  // op 5 (op 0 keeping g and u in 8 bits, 256 x 256 tiles only): keep_g and keep_u take the
+  // int8 codes [max_rows][n_out] and these the scale bytes [max_rows][ceil(n_out / 32)].
+  void* keep_sg;
+  void* keep_su;
 };
 // op 0: out = silu(a b0^T) * (a b1^T) (bf16 a, half out); op 1: out = a b0^T (bf16 a,
 // float32 out; with b_kmajor set in both problems, B read from K-major b0 / b1, 256 x 256
 // tiles only); op 2: out = a b0^T with a in half (the layer's h), float32 out; op 3: op 2
 // with the combine epilogue (comb_* fields), bf16 out, on the 256 x 256 tiles only (the
 // launch is refused where gemm_pair_uses_pp is false); op 4: op 0 keeping g and u
-// (keep_g / keep_u, IEEE half) with h in bf16 (256 x 256 tiles, roles 2 and 3). Both problems in one
-// launch.
+// (keep_g / keep_u, IEEE half) with h in bf16 (256 x 256 tiles, roles 2 and 3); op 5:
+// op 0 keeping the 8-bit checkpoints of g and u (256 x 256 tiles, role 2). Both problems
+// in one launch.
 // (float32 layers: op 2 is op 1.)
 // role names the launch in profiles: 0 standalone grouped, 1 standalone single
 // segment, 2 the layer's fused launch, 3 the layer backward.

@@ -4,8 +4,9 @@ owns the workspace and output buffers, and calls ``moe_layer_forward`` (and
 import numpy as np
 import torch
 
-from . import (AuxOut, LayerGrads, LayerParams, MOE_BF16, MOE_WS_BACKWARD, MOE_WS_LAYER, dims_from_config,
-               moe_layer_backward, moe_layer_backward_saved, moe_layer_forward, moe_layer_forward_train,
+from . import (AuxOut, LayerGrads, LayerParams, MOE_BF16, MOE_WS_BACKWARD, MOE_WS_LAYER, MOE_WS_STATE8,
+               MOE_WS_TRAIN8, dims_from_config, moe_layer_backward, moe_layer_backward_saved,
+               moe_layer_backward_saved8, moe_layer_forward, moe_layer_forward_train, moe_layer_forward_train8,
                workspace_bytes)
 
 
@@ -80,7 +81,7 @@ class MoeLayer:
 
     GRADS = ("dx", "dw_router", "dw_gate", "dw_up", "dw_down", "dws_gate", "dws_up", "dws_down")
 
-    def _backward_buffers(self):
+    def _gradient_buffers(self):
         if getattr(self, "grads", None) is None:
             cfg, dev, f32 = self.cfg, self.x.device, torch.float32
             N, d, F, Fs = cfg.n_experts, cfg.d_model, cfg.d_ff, cfg.d_ff_shared
@@ -90,10 +91,19 @@ class MoeLayer:
                           for k, v in shapes.items()}
             p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
             self.grads_struct = LayerGrads(*(p(self.grads[k]) for k in self.GRADS))
-            self.ws_bwd = torch.empty((max(workspace_bytes(self.dims, MOE_WS_BACKWARD), 256),),
-                                      dtype=torch.uint8, device=dev)
             self.aux_train = AuxOut(None, None, None, None, None, p(self.counts), None, p(self.P),
                                     p(self.scalars))
+
+    def _buffer(self, name, which):
+        """A byte buffer of the size the library names, allocated on first use."""
+        if getattr(self, name, None) is None:
+            setattr(self, name, torch.empty((max(workspace_bytes(self.dims, which), 256),), dtype=torch.uint8,
+                                            device=self.x.device))
+        return getattr(self, name)
+
+    def _backward_buffers(self):
+        self._gradient_buffers()
+        self._buffer("ws_bwd", MOE_WS_BACKWARD)
 
     def backward(self, dy, alpha=0.0, beta=0.0, stream=None):
         """Gradients of <dy, y> + alpha L_bal + beta L_z (float32 device tensors,
@@ -115,6 +125,23 @@ class MoeLayer:
         self._backward_buffers()
         moe_layer_backward_saved(self.dims, self.params, dy, alpha, beta, self.grads_struct, self.ws_bwd,
                                  stream=stream)
+        return self.grads
+
+    def forward_train8(self, ws=None, stream=None):
+        """forward_train() whose state is kept in 8 bits in self.state8; ws: scratch of
+        MOE_WS_TRAIN8 bytes, which layers of a model can share (its own by default)."""
+        self._gradient_buffers()
+        moe_layer_forward_train8(self.dims, self.params, self.y, self.aux_train,
+                                 self._buffer("state8", MOE_WS_STATE8),
+                                 self._buffer("ws_train8", MOE_WS_TRAIN8) if ws is None else ws, stream=stream)
+        return self.y
+
+    def backward_saved8(self, dy, alpha=0.0, beta=0.0, ws=None, stream=None):
+        """backward() from the state of the last forward_train8() call."""
+        self._gradient_buffers()
+        moe_layer_backward_saved8(self.dims, self.params, dy, alpha, beta, self.grads_struct,
+                                  self._buffer("state8", MOE_WS_STATE8),
+                                  self._buffer("ws_train8", MOE_WS_TRAIN8) if ws is None else ws, stream=stream)
         return self.grads
 
     def validate(self):
