@@ -161,7 +161,7 @@ _EMPTY = 256  # address of a tensor without elements (torch has none): nothing o
 
 def _device():
     """Index of the current device; tensors of these calls have to be on it."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 def _row_stream(stream, dev):

@@ -116,22 +116,79 @@ __device__ __forceinline__ float wave_sum(float v) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), 63));
 }
 
+// Gradient of the constant null expert's vector, sum over tokens of (sum of the null
+// slots' weights) dy_t: float32 sums over chunks of tokens, one wavefront per chunk and
+// 256 columns, then a float64 sum of the chunks in a fixed order. Short chunks for few
+// tokens keep the chip busy, longer ones for many keep the partial sums small next to dy.
+constexpr int kNullCols = 4;
+constexpr int null_chunk(int64_t T) { return T <= 4096 ? 16 : 64; }
+// The units (chunk, columns) of wavefront `wave` of nwaves.
+template <typename ET>
+__device__ __forceinline__ void null_vector_partial(const ET* __restrict__ dy, const int32_t* __restrict__ slot_pos,
+                                                    const float* __restrict__ topk_w, int64_t T, int K, int d,
+                                                    int64_t wave, int64_t nwaves, float* __restrict__ part) {
+  const int lane = threadIdx.x & (kWave - 1), chunk = null_chunk(T);
+  const int spans = (d + kWave * kNullCols - 1) / (kWave * kNullCols);
+  const int64_t chunks = (T + chunk - 1) / chunk;
+  for (int64_t unit = wave; unit < chunks * spans; unit += nwaves) {
+    const int64_t at = unit / spans, t0 = at * chunk;
+    const int n = (int)min<int64_t>(chunk, T - t0);
+    const int c = (int)(unit - at * spans) * kWave * kNullCols + lane * kNullCols;
+    float my_w = 0.0f;  // lane i: token t0 + i
+    bool any = false;
+    if (lane < n)
+      for (int k = 0; k < K; ++k)
+        if (slot_pos[(t0 + lane) * K + k] == kNullSlot) {
+          my_w += topk_w[(t0 + lane) * K + k];
+          any = true;
+        }
+    float acc[kNullCols] = {0.0f, 0.0f, 0.0f, 0.0f};
+    constexpr int kAhead = 8;
+    for (uint64_t todo = ballot(any); todo;) {
+      RawRow<ET, kNullCols> g[kAhead];
+      float w[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        w[i] = 0.0f;
+        g[i].zero();
+        if (todo) {
+          const int k = __builtin_ctzll(todo);
+          todo &= todo - 1;
+          w[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), k));
+          if (c < d) g[i].load(dy + (t0 + k) * d + c);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+        for (int j = 0; j < kNullCols; ++j) acc[j] = fmaf(w[i], g[i][j], acc[j]);
+    }
+    if (c < d) store_row<kNullCols>(part + at * d + c, acc);
+  }
+}
 // The combine's gradient: WPT wavefronts per token, each with every WPT-th span of
 // kSpan columns, whose parts of the slots' products meet in LDS. One wavefront per token
 // holds the whole row's loads in registers and so fewer of them over the chip (16384 x
-// 2048, 8 slots a quarter real, bf16: 106 us, 80 us with two slots at a time).
+// 2048, 8 slots a quarter real, bf16: 106 us, 80 us with two slots at a time, 70 us so).
+// The constant null vector's sums over token chunks run in workgroups of the same launch.
 template <typename RT, typename ET, int WPT>
 __global__ void __launch_bounds__(kThreads)
 combine_bwd_kernel(const ET* __restrict__ dy, const RT* __restrict__ y_perm, const int32_t* __restrict__ slot_pos,
                    const float* __restrict__ topk_w, const ET* __restrict__ null_src, int64_t null_stride,
                    RT* __restrict__ dy_perm, float* __restrict__ w_perm, int32_t* __restrict__ row_slot,
                    float* __restrict__ dtopk_w, float* __restrict__ dnull, int64_t T, int K, int d,
-                   int64_t max_rows) {
+                   int64_t max_rows, unsigned blocks, float* __restrict__ null_part) {
   constexpr int kTokens = kThreads / kWave / WPT;  // tokens per workgroup
+  if (blockIdx.x >= blocks) {  // the workgroups behind those of the tokens
+    constexpr int kWaves = kThreads / kWave;
+    null_vector_partial(dy, slot_pos, topk_w, T, K, d, (int64_t)(blockIdx.x - blocks) * kWaves + threadIdx.x / kWave,
+                        (int64_t)(gridDim.x - blocks) * kWaves, null_part);
+    return;
+  }
   __shared__ float part[kThreads / kWave][MOE_MAX_TOPK];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, sub = wave % WPT;
   const bool dots = y_perm && dtopk_w;
-  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < T; t0 += (int64_t)gridDim.x * kTokens) {
+  for (int64_t t0 = (int64_t)blockIdx.x * kTokens; t0 < T; t0 += (int64_t)blocks * kTokens) {
     const int64_t t = t0 + wave / WPT;
     int my_p = kNoSlot;
     float my_w = 0.0f, my_dot = 0.0f;  // lane k: slot k
@@ -224,58 +281,6 @@ combine_bwd_kernel(const ET* __restrict__ dy, const RT* __restrict__ y_perm, con
   }
 }
 
-// Gradient of the constant null expert's vector, sum over tokens of (sum of the null
-// slots' weights) dy_t: float32 sums over chunks of tokens, one wavefront per chunk and
-// 256 columns, then a float64 sum of the chunks in a fixed order. Short chunks for few
-// tokens keep the chip busy, longer ones for many keep the partial sums small next to dy.
-constexpr int kNullCols = 4;
-constexpr int kMaxNullChunk = 64;
-constexpr int null_chunk(int64_t T) { return T <= 4096 ? 16 : kMaxNullChunk; }
-template <typename ET>
-__global__ void __launch_bounds__(kThreads)
-null_vector_partial_kernel(const ET* __restrict__ dy, const int32_t* __restrict__ slot_pos,
-                           const float* __restrict__ topk_w, int64_t T, int K, int d, int chunk, int64_t chunks,
-                           float* __restrict__ part) {
-  const int lane = threadIdx.x & (kWave - 1);
-  const int spans = (d + kWave * kNullCols - 1) / (kWave * kNullCols);
-  const int64_t nwaves = (int64_t)gridDim.x * (kThreads / kWave);
-  for (int64_t unit = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; unit < chunks * spans;
-       unit += nwaves) {
-    const int64_t at = unit / spans, t0 = at * chunk;
-    const int n = (int)min<int64_t>(chunk, T - t0);
-    const int c = (int)(unit - at * spans) * kWave * kNullCols + lane * kNullCols;
-    float my_w = 0.0f;  // lane i: token t0 + i
-    bool any = false;
-    if (lane < n)
-      for (int k = 0; k < K; ++k)
-        if (slot_pos[(t0 + lane) * K + k] == kNullSlot) {
-          my_w += topk_w[(t0 + lane) * K + k];
-          any = true;
-        }
-    float acc[kNullCols] = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kAhead = 8;
-    for (uint64_t todo = ballot(any); todo;) {
-      RawRow<ET, kNullCols> g[kAhead];
-      float w[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        w[i] = 0.0f;
-        g[i].zero();
-        if (todo) {
-          const int k = __builtin_ctzll(todo);
-          todo &= todo - 1;
-          w[i] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(my_w), k));
-          if (c < d) g[i].load(dy + (t0 + k) * d + c);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-        for (int j = 0; j < kNullCols; ++j) acc[j] = fmaf(w[i], g[i][j], acc[j]);
-    }
-    if (c < d) store_row<kNullCols>(part + at * d + c, acc);
-  }
-}
 // 64 columns per workgroup, chunks over its 16 wavefronts.
 constexpr int kReduceWaves = 16;
 __global__ void __launch_bounds__(kReduceWaves * kWave)
@@ -336,27 +341,25 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
   auto typed = [&](auto* r, auto* e) {
     typedef std::remove_pointer_t<decltype(r)> RT;
     typedef std::remove_pointer_t<decltype(e)> ET;
-    float* dnull = a.null_stride ? a.dnull : nullptr;  // per token; the constant's follows
+    float* dnull = a.null_stride ? a.dnull : nullptr;  // per token (copy)
+    const bool vector = a.dnull && !a.null_stride;     // one vector (constant)
+    const int chunk = null_chunk(a.T);
+    const int64_t chunks = (a.T + chunk - 1) / chunk;
+    const int spans = (a.d + kWave * kNullCols - 1) / (kWave * kNullCols);
+    const unsigned extra = vector ? (unsigned)std::min<int64_t>((chunks * spans + 3) / 4, 1 << 20) : 0;
     auto go = [&](auto wpt) {
       constexpr int WPT = decltype(wpt)::value, kTokens = kThreads / kWave / WPT;
       const unsigned blocks = (unsigned)std::min<int64_t>((a.T + kTokens - 1) / kTokens, 1 << 20);
-      combine_bwd_kernel<RT, ET, WPT><<<blocks, kThreads, 0, stream>>>(
+      combine_bwd_kernel<RT, ET, WPT><<<blocks + extra, kThreads, 0, stream>>>(
           static_cast<const ET*>(a.dy), static_cast<const RT*>(a.y_perm), a.slot_pos, a.topk_w,
           static_cast<const ET*>(a.null_src), a.null_stride, static_cast<RT*>(a.dy_perm), a.w_perm, a.row_slot,
-          a.dtopk_w, dnull, a.T, a.K, a.d, a.max_rows);
+          a.dtopk_w, dnull, a.T, a.K, a.d, a.max_rows, blocks, a.part);
     };
     if (a.d <= kSpan) go(std::integral_constant<int, 1>{});
     else if (a.d <= 2 * kSpan) go(std::integral_constant<int, 2>{});
     else go(std::integral_constant<int, 4>{});
-    hipError_t err = hipGetLastError();
-    if (err != hipSuccess || !a.dnull || a.null_stride) return err;
-    const int chunk = null_chunk(a.T);
-    const int64_t chunks = (a.T + chunk - 1) / chunk;
-    const int spans = (a.d + kWave * kNullCols - 1) / (kWave * kNullCols);
-    null_vector_partial_kernel<ET><<<(unsigned)std::min<int64_t>((chunks * spans + 3) / 4, 1 << 20), kThreads, 0,
-                                     stream>>>(static_cast<const ET*>(a.dy), a.slot_pos, a.topk_w, a.T, a.K, a.d,
-                                               chunk, chunks, a.part);
-    if ((err = hipGetLastError()) != hipSuccess) return err;
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess || !vector) return err;
     null_vector_reduce_kernel<<<(unsigned)((a.d + kWave - 1) / kWave), kReduceWaves * kWave, 0, stream>>>(
         a.part, chunks, a.d, a.dnull);
     return hipGetLastError();
