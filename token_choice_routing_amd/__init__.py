@@ -185,16 +185,18 @@ def _refuse(name, t, dev, dtype, shape):
     raise ValueError(f"{name}: expected a contiguous tensor")
 
 
-def _arg(name, t, dev, dtype, shape=None):
+def _arg(name, t, dev, dtype, shape):
     """Device address of a dense tensor whose type and shape the call fixes: the library
     sees addresses only, so another type, shape or device is refused here."""
-    if not (isinstance(t, torch.Tensor) and t.get_device() == dev and t.dtype is dtype
-            and (shape is None or t.shape == shape) and t.is_contiguous()):
-        _refuse(name, t, dev, dtype, shape)
-    return t.data_ptr() or _EMPTY
+    try:
+        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+            return t.data_ptr() or _EMPTY
+    except AttributeError:
+        pass
+    _refuse(name, t, dev, dtype, shape)
 
 
-def _opt(name, t, dev, dtype, shape=None):
+def _opt(name, t, dev, dtype, shape):
     return None if t is None else _arg(name, t, dev, dtype, shape)
 
 
@@ -205,11 +207,11 @@ def _matrix(name, t, dev, dtype=None, shape=None):
         raise ValueError(f"{name}: expected a matrix of float32, bfloat16 or float16")
     if t.get_device() != dev or (dtype is not None and t.dtype is not dtype) or (shape is not None and t.shape != shape):
         _refuse(name, t, dev, dtype or t.dtype, shape)
-    if t.is_contiguous():
-        return t.data_ptr() or _EMPTY, t.shape[1]
+    ld, inner = t.stride()
     rows, cols = t.shape
-    ld = t.stride(0) if rows > 1 else cols
-    if (cols > 1 and t.stride(1) != 1) or ld < cols:
+    if rows <= 1:
+        ld = cols
+    if (inner != 1 and cols > 1) or ld < cols:
         raise ValueError(f"{name}: expected rows that are dense and do not overlap, got strides {t.stride()}")
     return t.data_ptr() or _EMPTY, ld
 
@@ -369,9 +371,7 @@ def act8_scales_shape(rows, cols):
     return rows, -(-cols // ACT8_BLOCK)
 
 
-def _kept(dev, shape, codes, scales, name=""):
-    return (_arg(name + "codes", codes, dev, torch.int8, shape),
-            _arg(name + "scales", scales, dev, torch.uint8, (shape[0], -(-shape[1] // ACT8_BLOCK))))
+_COUNT = (1,)
 
 
 def moe_act8_pack(x, codes, scales, n_rows=None, stream=None):
@@ -381,9 +381,11 @@ def moe_act8_pack(x, codes, scales, n_rows=None, stream=None):
     dev = _device()
     px, ld = _matrix("x", x, dev)
     shape = x.shape
-    pc, ps = _kept(dev, shape, codes, scales)
+    scaled = (shape[0], -(-shape[1] // ACT8_BLOCK))
     _check(load_library().moe_act8_pack(shape[0], shape[1], _ROW_TYPES[x.dtype], px, ld,
-                                        _opt("n_rows", n_rows, dev, torch.int32, (1,)), pc, ps,
+                                        _opt("n_rows", n_rows, dev, torch.int32, _COUNT),
+                                        _arg("codes", codes, dev, torch.int8, shape),
+                                        _arg("scales", scales, dev, torch.uint8, scaled),
                                         _row_stream(stream, dev)), "moe_act8_pack")
 
 
@@ -392,9 +394,11 @@ def moe_act8_unpack(codes, scales, out, n_rows=None, stream=None):
     dev = _device()
     po, ld = _matrix("out", out, dev)
     shape = out.shape
-    pc, ps = _kept(dev, shape, codes, scales)
-    _check(load_library().moe_act8_unpack(shape[0], shape[1], _ROW_TYPES[out.dtype], pc, ps,
-                                          _opt("n_rows", n_rows, dev, torch.int32, (1,)), po, ld,
+    scaled = (shape[0], -(-shape[1] // ACT8_BLOCK))
+    _check(load_library().moe_act8_unpack(shape[0], shape[1], _ROW_TYPES[out.dtype],
+                                          _arg("codes", codes, dev, torch.int8, shape),
+                                          _arg("scales", scales, dev, torch.uint8, scaled),
+                                          _opt("n_rows", n_rows, dev, torch.int32, _COUNT), po, ld,
                                           _row_stream(stream, dev)), "moe_act8_unpack")
 
 
@@ -407,10 +411,12 @@ def moe_swiglu_keep8(g, u, h, g_codes, g_scales, u_codes, u_scales, n_rows=None,
     pu, ldu = _matrix("u", u, dev, dt, shape)
     if ld != ldu:
         raise ValueError(f"g and u: expected the same spacing of rows, got {ld} and {ldu}")
+    i8, u8, scaled = torch.int8, torch.uint8, (shape[0], -(-shape[1] // ACT8_BLOCK))
     _check(load_library().moe_swiglu_keep8(
-        shape[0], shape[1], _ROW_TYPES[dt], pg, pu, ld, _opt("n_rows", n_rows, dev, torch.int32, (1,)),
-        _arg("h", h, dev, dt, shape), *_kept(dev, shape, g_codes, g_scales, "g_"),
-        *_kept(dev, shape, u_codes, u_scales, "u_"), _row_stream(stream, dev)), "moe_swiglu_keep8")
+        shape[0], shape[1], _ROW_TYPES[dt], pg, pu, ld, _opt("n_rows", n_rows, dev, torch.int32, _COUNT),
+        _arg("h", h, dev, dt, shape), _arg("g_codes", g_codes, dev, i8, shape),
+        _arg("g_scales", g_scales, dev, u8, scaled), _arg("u_codes", u_codes, dev, i8, shape),
+        _arg("u_scales", u_scales, dev, u8, scaled), _row_stream(stream, dev)), "moe_swiglu_keep8")
 
 
 def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=None, w_rows=None, dw=None,
@@ -424,18 +430,23 @@ def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=Non
     pu, ldu = _matrix("du", du, dev, dt, shape)
     if ld != ldu:
         raise ValueError(f"dg and du: expected the same spacing of rows, got {ld} and {ldu}")
-    pd, ldd = _matrix("dh", dh, dev, None, shape)
-    if ldd != shape[1]:
-        raise ValueError("dh: expected a contiguous tensor")
-    n_slots = 0 if dw is None else dw.numel()
-    if dw is not None and row_slot is None and n_slots != shape[0]:
-        raise ValueError(f"dw: expected {shape[0]} elements, got {n_slots}")
+    tdh = getattr(dh, "dtype", None)
+    if tdh not in _ROW_TYPES:
+        raise ValueError("dh: expected a matrix of float32, bfloat16 or float16")
+    n_slots, pw = 0, None
+    if dw is not None:
+        n_slots = dw.numel()
+        if row_slot is None and n_slots != shape[0]:
+            raise ValueError(f"dw: expected {shape[0]} elements, got {n_slots}")
+        pw = _arg("dw", dw, dev, f32, dw.shape)
+    i8, u8, scaled = torch.int8, torch.uint8, (shape[0], -(-shape[1] // ACT8_BLOCK))
     _check(load_library().moe_swiglu_backward8(
-        shape[0], shape[1], *_kept(dev, shape, g_codes, g_scales, "g_"), *_kept(dev, shape, u_codes, u_scales, "u_"),
-        _opt("n_rows", n_rows, dev, torch.int32, (1,)), _ROW_TYPES[dh.dtype], pd,
-        _opt("w_rows", w_rows, dev, f32, (shape[0],)), _opt("row_slot", row_slot, dev, torch.int32, (shape[0],)),
-        n_slots, _ROW_TYPES[dt], pg, pu, ld, _opt("h", h, dev, dt, shape), _opt("dw", dw, dev, f32),
-        _row_stream(stream, dev)), "moe_swiglu_backward8")
+        shape[0], shape[1], _arg("g_codes", g_codes, dev, i8, shape), _arg("g_scales", g_scales, dev, u8, scaled),
+        _arg("u_codes", u_codes, dev, i8, shape), _arg("u_scales", u_scales, dev, u8, scaled),
+        _opt("n_rows", n_rows, dev, torch.int32, _COUNT), _ROW_TYPES[tdh], _arg("dh", dh, dev, tdh, shape),
+        _opt("w_rows", w_rows, dev, f32, shape[:1]), _opt("row_slot", row_slot, dev, torch.int32, shape[:1]),
+        n_slots, _ROW_TYPES[dt], pg, pu, ld, _opt("h", h, dev, dt, shape), pw, _row_stream(stream, dev)),
+        "moe_swiglu_backward8")
 
 
 def moe_aux_stats(dims, logits, topk_idx, f, P, counts, scalars, ws, stream=None):
