@@ -269,7 +269,9 @@ def _within(got, ref, tol, what):
 SWIGLU = [(1, 8, "bf16", "bf16", "bf16", False), (5, 40, "f32", "f32", "f32", True),
           (33, 136, "f16", "f16", "f16", True), (130, 776, "bf16", "f32", "bf16", True),
           (64, 1536, "bf16", "bf16", "bf16", False), (7, 4104, "f32", "bf16", "f32", True),
-          (300, 264, "f16", "f32", "bf16", False)]
+          (300, 264, "f16", "f32", "bf16", False),
+          # many rows take one wavefront each, few long ones four
+          (2100, 528, "bf16", "bf16", "bf16", True), (3, 2056, "f16", "f32", "f32", True)]
 
 
 @pytest.mark.parametrize("rows,F,act,dht,out,weighted", SWIGLU)
@@ -321,8 +323,8 @@ def test_swiglu8(rows, F, act, dht, out, weighted):
         assert torch.equal(dgu2, dgu)
 
 
-def test_swiglu8_live_rows():
-    rows, F, m = 12, 104, 5
+@pytest.mark.parametrize("rows,F,m", [(12, 104, 5), (12, 1048, 5), (2500, 520, 2049), (6, 1048, 0)])
+def test_swiglu8_live_rows(rows, F, m):
     rng = np.random.default_rng(2)
     g, u, dh = (rounded(rng, (rows, F), "bf16")[0] for _ in range(3))
     g[m:] = float("nan")
@@ -333,7 +335,7 @@ def test_swiglu8_live_rows():
 
     h, h8, dg, du = (fresh() for _ in range(4))
     cg, cu = fresh(torch.int8), fresh(torch.int8)
-    sg, su = (torch.full((rows, 4), 7, dtype=torch.uint8, device="cuda") for _ in range(2))
+    sg, su = (torch.full(tcr.act8_scales_shape(rows, F), 7, dtype=torch.uint8, device="cuda") for _ in range(2))
     dw = torch.full((rows,), 7.0, device="cuda")
     tcr.moe_swiglu_keep8(g, u, h, cg, sg, cu, su, n_rows=n)
     tcr.moe_swiglu_backward8(cg, sg, cu, su, dh, dg, du, h=h8, dw=dw, n_rows=n)

@@ -206,23 +206,38 @@ swiglu_bwd8_kernel(Bwd8 a, RowMap m, const DT* __restrict__ dh, OT* __restrict__
   });
 }
 
-// Rows with weight gradients dw = <dh, h>: one wavefront per row, lane sums added in a
-// fixed order.
-template <typename DT, typename OT>
+// Rows with weight gradients dw = <dh, h>: WPR wavefronts per row, whose lane sums are
+// added in a fixed order. Four of them for few rows, which leave most of the chip's
+// wavefronts free (bf16, us with one against four: 1 x 1536 5.4 and 3.4, 1024 x 1536 7.6
+// and 6.3, 64 x 14336 35 and 11); one for many, without the join (4096 x 1536 14.2 and
+// 15.3, 32768 x 1536 96 and 106).
+constexpr int64_t kFewRows = 2048;
+template <typename DT, typename OT, int WPR>
 __global__ void __launch_bounds__(kThreads)
 swiglu_bwd8_row_kernel(Bwd8 a, const DT* __restrict__ dh, OT* __restrict__ dg, OT* __restrict__ du,
                        OT* __restrict__ h) {
-  const int lane = threadIdx.x & (kWave - 1);
+  constexpr int kWaves = kThreads / kWave, kRows = kWaves / WPR;  // rows per workgroup
+  __shared__ float part[kWaves];
+  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, sub = wave % WPR;
   const int64_t n = live_rows(a.n_rows, a.rows), nb = (a.F + 31) / 32;
-  const int64_t nwaves = (int64_t)gridDim.x * (kThreads / kWave);
-  for (int64_t row = (int64_t)blockIdx.x * (kThreads / kWave) + threadIdx.x / kWave; row < n; row += nwaves) {
-    const float w = a.w_rows ? a.w_rows[row] : 1.0f;
+  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < n; row0 += (int64_t)gridDim.x * kRows) {
+    const int64_t row = row0 + wave / WPR;
     float dot = 0.0f;
-    for (int64_t col = lane * kCols; col < a.F; col += kWave * kCols)
-      dot += swiglu_bwd8_step(a, dh, dg, du, h, nb, row, col, w);
+    if (row < n) {
+      const float w = a.w_rows ? a.w_rows[row] : 1.0f;
+      for (int64_t col = (sub * kWave + lane) * kCols; col < a.F; col += WPR * kWave * kCols)
+        dot += swiglu_bwd8_step(a, dh, dg, du, h, nb, row, col, w);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
-    if (lane == 0) {
+      for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
+    }
+    if (WPR > 1) {
+      if (lane == 0) part[wave] = dot;
+      __syncthreads();
+      if (sub == 0)
+        for (int i = 1; i < WPR; ++i) dot += part[wave + i];
+      __syncthreads();
+    }
+    if (row < n && sub == 0 && lane == 0) {
       const int64_t to = a.row_slot ? a.row_slot[row] : row;
       if (to >= 0 && to < a.n_slots) a.dw[to] = dot;
     }
@@ -291,8 +306,12 @@ hipError_t launch_swiglu_bwd8(const SwigluBwd8Args& a, hipStream_t s) {
       const DT* dh = static_cast<const DT*>(a.dh);
       OT *dg = static_cast<OT*>(a.dg), *du = static_cast<OT*>(a.du), *h = static_cast<OT*>(a.h);
       if (a.dw) {
-        const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + 3) / 4, 1 << 20);
-        swiglu_bwd8_row_kernel<DT, OT><<<blocks, kThreads, 0, s>>>(b, dh, dg, du, h);
+        if (a.rows <= kFewRows && a.F > kWave * kCols) {
+          swiglu_bwd8_row_kernel<DT, OT, 4><<<(unsigned)a.rows, kThreads, 0, s>>>(b, dh, dg, du, h);
+        } else {
+          const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + 3) / 4, 1 << 20);
+          swiglu_bwd8_row_kernel<DT, OT, 1><<<blocks, kThreads, 0, s>>>(b, dh, dg, du, h);
+        }
       } else {
         swiglu_bwd8_kernel<DT, OT><<<grid_of(a.rows, m), kThreads, 0, s>>>(b, m, dh, dg, du, h);
       }
