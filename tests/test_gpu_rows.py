@@ -344,3 +344,73 @@ def test_swiglu8_live_rows(rows, F, m):
     whole = [fresh() for _ in range(3)]
     tcr.moe_swiglu_backward8(cg, sg, cu, su, dh, whole[0], whole[1], h=whole[2])
     assert all(torch.equal(a[:m], b[:m]) for a, b in zip(whole, (dg, du, h8)))
+
+
+def test_binding_refusals():
+    """Tensors of another type, shape or layout than the call fixes are refused before it."""
+    D = dims(6, 64, 8, 2, "bf16")
+    x, rows = (torch.zeros((n, 64), dtype=torch.bfloat16, device="cuda") for n in (6, 12))
+    sp, w = torch.zeros((6, 2), dtype=torch.int32, device="cuda"), torch.zeros((6, 2), device="cuda")
+    B, F = tcr.MOE_BF16, tcr.MOE_F32
+    wide = torch.zeros((12, 128), dtype=torch.bfloat16, device="cuda")[:, :64]
+    for bad in (rows.float(), rows[:11], wide, rows.cpu()):
+        with pytest.raises(ValueError, match="y_perm"):
+            tcr.moe_combine_rows(D, B, bad, sp, w, None, x)
+        with pytest.raises(ValueError, match="dx_perm"):
+            tcr.moe_permute_backward(D, B, bad, sp, None, B, x)
+        with pytest.raises(ValueError, match="dy_perm"):
+            tcr.moe_combine_backward(D, B, x, rows, sp, w, dy_perm=bad)
+    for bad in (sp.long(), sp[:5], sp.t().contiguous().t()):
+        with pytest.raises(ValueError, match="slot_pos"):
+            tcr.moe_combine_rows(D, B, rows, bad, w, None, x)
+    with pytest.raises(ValueError, match="rows_dtype"):
+        tcr.moe_combine_rows(D, 5, rows, sp, w, None, x)
+    with pytest.raises(tcr.MoeError):
+        tcr.moe_combine_rows(D, B, None, sp, w, None, x)
+    with pytest.raises(ValueError, match="row_slot"):
+        tcr.moe_combine_backward(D, B, x, rows, sp, w, row_slot=torch.zeros((12,), device="cuda"))
+    with pytest.raises(ValueError, match="dx"):
+        tcr.moe_permute_backward(D, F, rows.float(), sp, None, F, x)
+    a, c, s = torch.zeros((5, 40), device="cuda"), torch.zeros((5, 40), dtype=torch.int8, device="cuda"), None
+    s = torch.zeros((5, 2), dtype=torch.uint8, device="cuda")
+    for args in ((a.double(), c, s), (a[0], c, s), (a.t(), c, s), (a, c[:4], s), (a, c, s[:, :1]), (a, c.float(), s),
+                 (a.cpu(), c, s), (a.expand(5, 40)[:, ::2], c, s), (a[:1].expand(5, 40), c, s)):
+        with pytest.raises(ValueError):
+            tcr.moe_act8_pack(*args)
+        with pytest.raises(ValueError):
+            tcr.moe_act8_unpack(args[1], args[2], args[0])
+    with pytest.raises(ValueError, match="n_rows"):
+        tcr.moe_act8_pack(a, c, s, n_rows=torch.zeros((1,), dtype=torch.int64, device="cuda"))
+    with pytest.raises(tcr.MoeError):  # rows spaced by no multiple of 8
+        tcr.moe_act8_pack(torch.zeros((5, 44), device="cuda")[:, :40], c, s)
+    with pytest.raises(tcr.MoeError):  # columns no multiple of 8
+        tcr.moe_act8_pack(torch.zeros((5, 44), device="cuda"), torch.zeros((5, 44), dtype=torch.int8, device="cuda"), s)
+    gu = torch.zeros((5, 80), device="cuda")
+    with pytest.raises(ValueError, match="spacing"):
+        tcr.moe_swiglu_keep8(gu[:, :40], a, a, c, s, c, s)
+    with pytest.raises(ValueError, match="h:"):
+        tcr.moe_swiglu_keep8(a, a, a.half(), c, s, c, s)
+    with pytest.raises(ValueError, match="dw"):
+        tcr.moe_swiglu_backward8(c, s, c, s, a, a, a, dw=torch.zeros((4,), device="cuda"))
+    with pytest.raises(ValueError, match="dh"):
+        tcr.moe_swiglu_backward8(c, s, c, s, gu[:, :40], a, a)
+    with pytest.raises(ValueError, match="w_rows"):
+        tcr.moe_swiglu_backward8(c, s, c, s, a, a, a, w_rows=torch.zeros((4,), device="cuda"))
+
+
+def test_no_rows():
+    """No tokens and no rows: accepted, nothing written."""
+    D = dims(0, 64, 8, 2, "bf16", "constant")
+    e = lambda *s, dtype=torch.bfloat16: torch.zeros(s, dtype=dtype, device="cuda")  # noqa: E731
+    v, dn = e(64), torch.full((64,), 7.0, device="cuda")
+    sp, w = e(0, 2, dtype=torch.int32), e(0, 2, dtype=torch.float32)
+    tcr.moe_combine_rows(D, tcr.MOE_BF16, e(0, 64), sp, w, None, e(0, 64), null_src=v)
+    tcr.moe_combine_backward(D, tcr.MOE_BF16, e(0, 64), e(0, 64), sp, w, e(0, 64), null_src=v, dnull=dn, ws=e(256))
+    tcr.moe_permute_backward(D, tcr.MOE_BF16, e(0, 64), sp, None, tcr.MOE_BF16, e(0, 64))
+    c, s = e(0, 64, dtype=torch.int8), e(0, 2, dtype=torch.uint8)
+    tcr.moe_act8_pack(e(0, 64), c, s)
+    tcr.moe_act8_unpack(c, s, e(0, 64))
+    tcr.moe_swiglu_keep8(e(0, 64), e(0, 64), e(0, 64), c, s, c, s)
+    tcr.moe_swiglu_backward8(c, s, c, s, e(0, 64), e(0, 64), e(0, 64), dw=e(0, dtype=torch.float32))
+    torch.cuda.synchronize()
+    assert bool((dn == 7.0).all())

@@ -11,6 +11,7 @@ pointers are shared). The library must have been built
 fall back to anything when it is missing.
 """
 import ctypes
+import importlib
 import os
 import re
 
@@ -18,6 +19,7 @@ import torch
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe_mi355x.so")
+MARSHAL_PATH = os.path.join(HERE, "_marshal.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "moe.h")
 
 MOE_OK, MOE_ERR_ARG, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_UNSUPPORTED, MOE_ERR_HIP, MOE_ERR_NONFINITE = range(7)
@@ -59,15 +61,17 @@ class LayerGrads(ctypes.Structure):
 
 
 _lib = None
+_marshal = None  # argument checks of the row operators (csrc/marshal.cpp), loaded with the library
 _P = ctypes.c_void_p
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
-    global _lib
+    global _lib, _marshal
     if _lib is not None:
         return _lib
-    if not os.path.exists(path):
+    if not os.path.exists(path) or not os.path.exists(MARSHAL_PATH):
         raise ImportError(f"{path} is not built; run `python -m token_choice_routing_amd.build`")
+    _marshal = importlib.import_module("._marshal", __name__)
     lib = ctypes.CDLL(path)
     D, I, L = ctypes.POINTER(Dims), ctypes.c_int32, ctypes.c_int64
     sig = {
@@ -152,12 +156,13 @@ def _stream(stream):
 
 _ROW_TYPES = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.float16: MOE_F16}
 _DTYPES = {v: k for k, v in _ROW_TYPES.items()}
-_EMPTY = 256  # address of a tensor without elements (torch has none): nothing of it is accessed
 
 
-# The calls below move rows and often take microseconds on the device, so their
-# arguments are checked in few steps: one device query per call, and per tensor one test
-# that passes for a right argument; what is wrong is worked out only when it fails.
+# The calls below move rows and often take microseconds on the device, about as long as
+# it takes to ask ten tensors from Python what they are: their arguments are checked in
+# one native call, and what is wrong is worked out only when it refuses one. The library
+# sees addresses only, so a tensor of another type or shape or on another device than the
+# current one is refused here.
 
 def _device():
     """Index of the current device; tensors of these calls have to be on it."""
@@ -171,49 +176,41 @@ def _row_stream(stream, dev):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-def _refuse(name, t, dev, dtype, shape):
-    if t is None:
-        raise ValueError(f"{name} is required")
+def _refuse(name, t, dev, dtype, shape, layout="a contiguous tensor"):
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name}: expected a tensor, got {type(t).__name__}")
     if t.get_device() != dev:
         raise ValueError(f"{name}: expected a tensor on the current device (cuda:{dev}), got one on {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    raise ValueError(f"{name}: expected a contiguous tensor")
+    raise ValueError(f"{name}: expected {layout}, got strides {t.stride()}")
 
 
-def _arg(name, t, dev, dtype, shape):
-    """Device address of a dense tensor whose type and shape the call fixes: the library
-    sees addresses only, so another type, shape or device is refused here."""
-    try:
-        if t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
-            return t.data_ptr() or _EMPTY
-    except AttributeError:
-        pass
-    _refuse(name, t, dev, dtype, shape)
+def _dense(dev, names, *spec):
+    """Device addresses of dense tensors; spec: a tensor (or None), its type and its shape
+    for each name."""
+    got = _marshal.dense(dev, *spec)
+    if got.__class__ is int:
+        _refuse(names[got], spec[3 * got], dev, spec[3 * got + 1], spec[3 * got + 2])
+    return got
 
 
-def _opt(name, t, dev, dtype, shape):
-    return None if t is None else _arg(name, t, dev, dtype, shape)
-
-
-def _matrix(name, t, dev, dtype=None, shape=None):
+def _matrix(name, t, dev, dtype, shape):
     """(device address, elements from row to row) of a [rows][cols] tensor whose rows may
     be spaced (a column range of a wider matrix) but are dense inside."""
-    if t is None or t.dim() != 2 or t.dtype not in _ROW_TYPES:
+    got = _marshal.matrix(dev, t, dtype, shape)
+    if got is None:
+        _refuse(name, t, dev, dtype, shape, "rows that are dense and do not overlap")
+    return got
+
+
+def _matrix_like(name, t):
+    """(type, shape) of a matrix that sets them for its call's other tensors."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.dtype not in _ROW_TYPES:
         raise ValueError(f"{name}: expected a matrix of float32, bfloat16 or float16")
-    if t.get_device() != dev or (dtype is not None and t.dtype is not dtype) or (shape is not None and t.shape != shape):
-        _refuse(name, t, dev, dtype or t.dtype, shape)
-    ld, inner = t.stride()
-    rows, cols = t.shape
-    if rows <= 1:
-        ld = cols
-    if (inner != 1 and cols > 1) or ld < cols:
-        raise ValueError(f"{name}: expected rows that are dense and do not overlap, got strides {t.stride()}")
-    return t.data_ptr() or _EMPTY, ld
+    return t.dtype, t.shape
 
 
 def _row_dtype(name, code):
@@ -317,18 +314,22 @@ def _slot_shapes(dims):
             (d,) if dims.null_kind == MOE_NULL_CONSTANT else (T, d))
 
 
+_COMBINE_ROWS = ("y_perm", "slot_pos", "topk_w", "y_shared", "null_src", "y")
+
+
 def moe_combine_rows(dims, rows_dtype, y_perm, slot_pos, topk_w, y_shared, y, null_src=None, stream=None):
     """moe_combine with y_perm and y_shared of type rows_dtype (MOE_F32, MOE_BF16 or
     MOE_F16). null_src: the rows a null slot adds (x for copy experts, v for constant)."""
-    dev, f32 = _device(), torch.float32
+    lib, dev = load_library(), _device()
     dt, token, slots, rows, nul = _slot_shapes(dims)
     rt = _row_dtype("rows_dtype", rows_dtype)
-    _check(load_library().moe_combine_rows(
-        ctypes.byref(dims), rows_dtype, _arg("y_perm", y_perm, dev, rt, rows),
-        _arg("slot_pos", slot_pos, dev, torch.int32, slots), _arg("topk_w", topk_w, dev, f32, slots),
-        _opt("y_shared", y_shared, dev, rt, token),
-        _opt("null_src", null_src, dev, dt, nul) if dims.null_kind else None,
-        _arg("y", y, dev, dt, token), _row_stream(stream, dev)), "moe_combine_rows")
+    ptrs = _dense(dev, _COMBINE_ROWS, y_perm, rt, rows, slot_pos, torch.int32, slots, topk_w, torch.float32, slots,
+                  y_shared, rt, token, null_src if dims.null_kind else None, dt, nul, y, dt, token)
+    _check(lib.moe_combine_rows(ctypes.byref(dims), rows_dtype, *ptrs, _row_stream(stream, dev)), "moe_combine_rows")
+
+
+_COMBINE_BACKWARD = ("dy", "y_perm", "slot_pos", "topk_w", "null_src", "dy_perm", "w_perm", "row_slot", "dtopk_w",
+                     "dnull")
 
 
 def moe_combine_backward(dims, rows_dtype, dy, y_perm, slot_pos, topk_w, dy_perm=None, w_perm=None, row_slot=None,
@@ -337,33 +338,36 @@ def moe_combine_backward(dims, rows_dtype, dy, y_perm, slot_pos, topk_w, dy_perm
     null source's dnull; w_perm and row_slot hold each expert row's weight and flat slot
     index. Every output is optional. ws: MOE_WS_COMBINE_BACKWARD bytes (constant nulls
     with dnull)."""
-    dev, f32, i32 = _device(), torch.float32, torch.int32
+    lib, dev, f32, i32 = load_library(), _device(), torch.float32, torch.int32
     dt, token, slots, rows, nul = _slot_shapes(dims)
     rt = _row_dtype("rows_dtype", rows_dtype)
-    null = dims.null_kind != MOE_NULL_ZERO
+    if not dims.null_kind:
+        null_src = dnull = None
+    ptrs = _dense(dev, _COMBINE_BACKWARD, dy, dt, token, y_perm, rt, rows, slot_pos, i32, slots, topk_w, f32, slots,
+                  null_src, dt, nul, dy_perm, rt, rows, w_perm, f32, rows[:1], row_slot, i32, rows[:1],
+                  dtopk_w, f32, slots, dnull, f32, nul)
     wp, wb = _ws(ws)
-    _check(load_library().moe_combine_backward(
-        ctypes.byref(dims), rows_dtype, _arg("dy", dy, dev, dt, token), _opt("y_perm", y_perm, dev, rt, rows),
-        _arg("slot_pos", slot_pos, dev, i32, slots), _arg("topk_w", topk_w, dev, f32, slots),
-        _opt("null_src", null_src, dev, dt, nul) if null else None, _opt("dy_perm", dy_perm, dev, rt, rows),
-        _opt("w_perm", w_perm, dev, f32, rows[:1]), _opt("row_slot", row_slot, dev, i32, rows[:1]),
-        _opt("dtopk_w", dtopk_w, dev, f32, slots), _opt("dnull", dnull, dev, f32, nul) if null else None,
-        wp, wb, _row_stream(stream, dev)), "moe_combine_backward")
+    _check(lib.moe_combine_backward(ctypes.byref(dims), rows_dtype, *ptrs, wp, wb, _row_stream(stream, dev)),
+           "moe_combine_backward")
+
+
+_PERMUTE_BACKWARD = ("dx_perm", "slot_pos", "dx_add", "dx")
 
 
 def moe_permute_backward(dims, rows_dtype, dx_perm, slot_pos, dx_add, dx_dtype, dx, stream=None):
     """Gradient of moe_permute's gather: dx = dx_add (float32, optional) + the sum of each
     token's real rows of dx_perm (rows_dtype), in dx_dtype; dx may be dx_add itself."""
-    dev = _device()
+    lib, dev = load_library(), _device()
     _, token, slots, rows, _ = _slot_shapes(dims)
     rt, dt = _row_dtype("rows_dtype", rows_dtype), _row_dtype("dx_dtype", dx_dtype)
-    _check(load_library().moe_permute_backward(
-        ctypes.byref(dims), rows_dtype, _arg("dx_perm", dx_perm, dev, rt, rows),
-        _arg("slot_pos", slot_pos, dev, torch.int32, slots), _opt("dx_add", dx_add, dev, torch.float32, token),
-        dx_dtype, _arg("dx", dx, dev, dt, token), _row_stream(stream, dev)), "moe_permute_backward")
+    pp, ps, pa, px = _dense(dev, _PERMUTE_BACKWARD, dx_perm, rt, rows, slot_pos, torch.int32, slots,
+                            dx_add, torch.float32, token, dx, dt, token)
+    _check(lib.moe_permute_backward(ctypes.byref(dims), rows_dtype, pp, ps, pa, dx_dtype, px,
+                                    _row_stream(stream, dev)), "moe_permute_backward")
 
 
 ACT8_BLOCK = 32  # columns that share a scale byte
+_COUNT = (1,)
 
 
 def act8_scales_shape(rows, cols):
@@ -371,52 +375,56 @@ def act8_scales_shape(rows, cols):
     return rows, -(-cols // ACT8_BLOCK)
 
 
-_COUNT = (1,)
+_ACT8 = ("n_rows", "codes", "scales")
 
 
 def moe_act8_pack(x, codes, scales, n_rows=None, stream=None):
     """8-bit checkpoint of x [rows][cols] (float32, bfloat16 or float16; rows may be
     spaced): codes int8 [rows][cols], scales uint8 [rows][ceil(cols / 32)]. n_rows: device
     int32 [1], the rows in use (all if None); the others are left as they were."""
-    dev = _device()
-    px, ld = _matrix("x", x, dev)
-    shape = x.shape
-    scaled = (shape[0], -(-shape[1] // ACT8_BLOCK))
-    _check(load_library().moe_act8_pack(shape[0], shape[1], _ROW_TYPES[x.dtype], px, ld,
-                                        _opt("n_rows", n_rows, dev, torch.int32, _COUNT),
-                                        _arg("codes", codes, dev, torch.int8, shape),
-                                        _arg("scales", scales, dev, torch.uint8, scaled),
-                                        _row_stream(stream, dev)), "moe_act8_pack")
+    lib, dev = load_library(), _device()
+    dt, shape = _matrix_like("x", x)
+    rows, cols = shape
+    px, ld = _matrix("x", x, dev, dt, shape)
+    pn, pc, ps = _dense(dev, _ACT8, n_rows, torch.int32, _COUNT, codes, torch.int8, shape,
+                        scales, torch.uint8, act8_scales_shape(rows, cols))
+    _check(lib.moe_act8_pack(rows, cols, _ROW_TYPES[dt], px, ld, pn, pc, ps, _row_stream(stream, dev)),
+           "moe_act8_pack")
 
 
 def moe_act8_unpack(codes, scales, out, n_rows=None, stream=None):
     """The values a checkpoint stands for, into out [rows][cols] (rows may be spaced)."""
-    dev = _device()
-    po, ld = _matrix("out", out, dev)
-    shape = out.shape
-    scaled = (shape[0], -(-shape[1] // ACT8_BLOCK))
-    _check(load_library().moe_act8_unpack(shape[0], shape[1], _ROW_TYPES[out.dtype],
-                                          _arg("codes", codes, dev, torch.int8, shape),
-                                          _arg("scales", scales, dev, torch.uint8, scaled),
-                                          _opt("n_rows", n_rows, dev, torch.int32, _COUNT), po, ld,
-                                          _row_stream(stream, dev)), "moe_act8_unpack")
+    lib, dev = load_library(), _device()
+    dt, shape = _matrix_like("out", out)
+    rows, cols = shape
+    po, ld = _matrix("out", out, dev, dt, shape)
+    pn, pc, ps = _dense(dev, _ACT8, n_rows, torch.int32, _COUNT, codes, torch.int8, shape,
+                        scales, torch.uint8, act8_scales_shape(rows, cols))
+    _check(lib.moe_act8_unpack(rows, cols, _ROW_TYPES[dt], pc, ps, pn, po, ld, _row_stream(stream, dev)),
+           "moe_act8_unpack")
+
+
+_KEEP8 = ("n_rows", "h", "g_codes", "g_scales", "u_codes", "u_scales")
 
 
 def moe_swiglu_keep8(g, u, h, g_codes, g_scales, u_codes, u_scales, n_rows=None, stream=None):
     """h = silu(g) u and the 8-bit checkpoints of g and u. g, u: [rows][d_ff] of one type,
     with the same spacing of rows; h: dense, the same type."""
-    dev = _device()
-    pg, ld = _matrix("g", g, dev)
-    shape, dt = g.shape, g.dtype
+    lib, dev, i8, u8 = load_library(), _device(), torch.int8, torch.uint8
+    dt, shape = _matrix_like("g", g)
+    rows, F = shape
+    pg, ld = _matrix("g", g, dev, dt, shape)
     pu, ldu = _matrix("u", u, dev, dt, shape)
     if ld != ldu:
         raise ValueError(f"g and u: expected the same spacing of rows, got {ld} and {ldu}")
-    i8, u8, scaled = torch.int8, torch.uint8, (shape[0], -(-shape[1] // ACT8_BLOCK))
-    _check(load_library().moe_swiglu_keep8(
-        shape[0], shape[1], _ROW_TYPES[dt], pg, pu, ld, _opt("n_rows", n_rows, dev, torch.int32, _COUNT),
-        _arg("h", h, dev, dt, shape), _arg("g_codes", g_codes, dev, i8, shape),
-        _arg("g_scales", g_scales, dev, u8, scaled), _arg("u_codes", u_codes, dev, i8, shape),
-        _arg("u_scales", u_scales, dev, u8, scaled), _row_stream(stream, dev)), "moe_swiglu_keep8")
+    scaled = act8_scales_shape(rows, F)
+    ptrs = _dense(dev, _KEEP8, n_rows, torch.int32, _COUNT, h, dt, shape, g_codes, i8, shape, g_scales, u8, scaled,
+                  u_codes, i8, shape, u_scales, u8, scaled)
+    _check(lib.moe_swiglu_keep8(rows, F, _ROW_TYPES[dt], pg, pu, ld, *ptrs, _row_stream(stream, dev)),
+           "moe_swiglu_keep8")
+
+
+_BACKWARD8 = ("g_codes", "g_scales", "u_codes", "u_scales", "n_rows", "dh", "w_rows", "row_slot", "h", "dw")
 
 
 def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=None, w_rows=None, dw=None,
@@ -424,29 +432,25 @@ def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=Non
     """The SwiGLU backward from the checkpoints of g and u: dg, du (one type, rows may be
     spaced alike), optionally h (the same type, dense) and dw = <dh, h> per row (at
     dw[row_slot[p]] when row_slot is given). w_rows scales dh per row in dg and du."""
-    dev, f32 = _device(), torch.float32
-    pg, ld = _matrix("dg", dg, dev)
-    shape, dt = dg.shape, dg.dtype
+    lib, dev, f32, i32, i8, u8 = load_library(), _device(), torch.float32, torch.int32, torch.int8, torch.uint8
+    dt, shape = _matrix_like("dg", dg)
+    rows, F = shape
+    pg, ld = _matrix("dg", dg, dev, dt, shape)
     pu, ldu = _matrix("du", du, dev, dt, shape)
     if ld != ldu:
         raise ValueError(f"dg and du: expected the same spacing of rows, got {ld} and {ldu}")
-    tdh = getattr(dh, "dtype", None)
-    if tdh not in _ROW_TYPES:
-        raise ValueError("dh: expected a matrix of float32, bfloat16 or float16")
-    n_slots, pw = 0, None
+    tdh, _ = _matrix_like("dh", dh)
+    n_slots, dw_shape = 0, None
     if dw is not None:
-        n_slots = dw.numel()
-        if row_slot is None and n_slots != shape[0]:
-            raise ValueError(f"dw: expected {shape[0]} elements, got {n_slots}")
-        pw = _arg("dw", dw, dev, f32, dw.shape)
-    i8, u8, scaled = torch.int8, torch.uint8, (shape[0], -(-shape[1] // ACT8_BLOCK))
-    _check(load_library().moe_swiglu_backward8(
-        shape[0], shape[1], _arg("g_codes", g_codes, dev, i8, shape), _arg("g_scales", g_scales, dev, u8, scaled),
-        _arg("u_codes", u_codes, dev, i8, shape), _arg("u_scales", u_scales, dev, u8, scaled),
-        _opt("n_rows", n_rows, dev, torch.int32, _COUNT), _ROW_TYPES[tdh], _arg("dh", dh, dev, tdh, shape),
-        _opt("w_rows", w_rows, dev, f32, shape[:1]), _opt("row_slot", row_slot, dev, torch.int32, shape[:1]),
-        n_slots, _ROW_TYPES[dt], pg, pu, ld, _opt("h", h, dev, dt, shape), pw, _row_stream(stream, dev)),
-        "moe_swiglu_backward8")
+        n_slots, dw_shape = dw.numel(), dw.shape
+        if row_slot is None and n_slots != rows:
+            raise ValueError(f"dw: expected {rows} elements, got {n_slots}")
+    scaled, col = act8_scales_shape(rows, F), (rows,)
+    cg, sg, cu, su, pn, pd, pw, pr, ph, pdw = _dense(
+        dev, _BACKWARD8, g_codes, i8, shape, g_scales, u8, scaled, u_codes, i8, shape, u_scales, u8, scaled,
+        n_rows, i32, _COUNT, dh, tdh, shape, w_rows, f32, col, row_slot, i32, col, h, dt, shape, dw, f32, dw_shape)
+    _check(lib.moe_swiglu_backward8(rows, F, cg, sg, cu, su, pn, _ROW_TYPES[tdh], pd, pw, pr, n_slots, _ROW_TYPES[dt],
+                                    pg, pu, ld, ph, pdw, _row_stream(stream, dev)), "moe_swiglu_backward8")
 
 
 def moe_aux_stats(dims, logits, topk_idx, f, P, counts, scalars, ws, stream=None):

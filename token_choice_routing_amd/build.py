@@ -1,9 +1,10 @@
-"""Builds libmoe_mi355x.so for gfx950 with hipcc, in-tree.
+"""Builds libmoe_mi355x.so for gfx950 with hipcc, and the binding's argument checks
+(_marshal.so) with g++ against torch's headers, in-tree.
 
     python -m token_choice_routing_amd.build
 
 Every call compiles all sources (one hipcc process per file, in parallel) and
-links the shared library next to this file.
+links the shared libraries next to this file.
 """
 import os
 import subprocess
@@ -17,6 +18,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "combine.hip", "aux.hip", "backward.hip", "validate.hip",
            "dispatch_grad.hip", "act8.hip"]
+MARSHAL = os.path.join(HERE, "_marshal.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 FLAGS = [
@@ -33,6 +35,20 @@ def _run(cmd):
     return r.returncode, out
 
 
+def _marshal_cmd(out):
+    """g++ line of the binding's argument checks (host code: Python and torch, no GPU)."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    return ["g++", "-O2", "-std=c++17", "-fPIC", "-shared",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-isystem", os.path.join(root, "include"),
+            "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+            "-isystem", sysconfig.get_paths()["include"], os.path.join(CSRC, "marshal.cpp"), "-o", out,
+            "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     objs, cmds = [], []
@@ -40,19 +56,21 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
         objs.append(obj)
         cmds.append([HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
+    cmds.append(_marshal_cmd(MARSHAL + ".tmp"))
     with ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 4, 8)) as ex:
         results = list(ex.map(_run, cmds))
     for cmd, (rc, out) in zip(cmds, results):
         if out.strip() and (verbose or rc):
             print(out, file=sys.stderr)
         if rc:
-            raise RuntimeError(f"hipcc failed: {' '.join(cmd)}")
+            raise RuntimeError(f"compiler failed: {' '.join(cmd)}")
     tmp = LIB + ".tmp"
     rc, out = _run([HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp, *objs])
     if rc:
         print(out, file=sys.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    os.replace(MARSHAL + ".tmp", MARSHAL)
     return LIB
 
 
