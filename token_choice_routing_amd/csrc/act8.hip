@@ -9,7 +9,7 @@
 // the code q (int8) stands for q 2^e, and the block's scale byte is e + 127: float32
 // exponent bits, so the scale and every product with it are exact and the codes do not
 // depend on how they are computed. |v - q 2^e| <= 2^(e-1), or 2^e where |v| > 127.5 2^e
-// is clamped; against the block's largest value that is at most 2^-7 (2^-6 clamped).
+// is clamped; either is at most 2^-7 of the block's largest value (64 to 128 steps).
 // int8 steps are uniform, so a block's error goes by its largest value; an 8-bit float
 // (4 significant bits) would be off by up to 2^-4 of that value itself. A block that
 // holds a NaN or an infinity has scale byte 255 and codes 0 and stands for NaN.
