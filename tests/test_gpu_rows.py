@@ -266,7 +266,8 @@ def _within(got, ref, tol, what):
     assert (np.abs(got - ref) <= tol).all(), f"{what}: worst {worst} of the tolerance"
 
 
-SWIGLU = [(1, 8, "bf16", "bf16", "bf16", False), (5, 40, "f32", "f32", "f32", True),
+SWIGLU = [(400, 64, "bf16", "f32", "bf16", True), (90, 256, "f32", "f32", "f32", True), (50, 512, "bf16", "bf16", "bf16", True),
+          (1, 8, "bf16", "bf16", "bf16", False), (5, 40, "f32", "f32", "f32", True),
           (33, 136, "f16", "f16", "f16", True), (130, 776, "bf16", "f32", "bf16", True),
           (64, 1536, "bf16", "bf16", "bf16", False), (7, 4104, "f32", "bf16", "f32", True),
           (300, 264, "f16", "f32", "bf16", False),

@@ -88,6 +88,8 @@ __device__ __forceinline__ void for_steps(const RowMap& m, int64_t rows, F&& f) 
   }
 }
 
+// (16384 x 2048 bf16: 25 us, 102 MB at 4.0 TB/s with both ends of the kernel; two or four
+// steps per thread 24.4)
 template <typename XT>
 __global__ void __launch_bounds__(kThreads)
 act8_pack_kernel(const XT* __restrict__ x, int64_t ldx, const int32_t* __restrict__ n_rows, int64_t rows, int cols,
@@ -102,6 +104,7 @@ act8_pack_kernel(const XT* __restrict__ x, int64_t ldx, const int32_t* __restric
   });
 }
 
+// (16384 x 2048 to bf16: 21 us, 102 MB at 4.9 TB/s)
 template <typename XT>
 __global__ void __launch_bounds__(kThreads)
 act8_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
@@ -125,6 +128,8 @@ __device__ __forceinline__ float sigmoid(float z) {
   return 1.0f / (1.0f + expf(-z));
 }
 
+// h and both checkpoints in one pass over g and u (32768 x 1536 bf16: 78 us, 406 MB at
+// 5.2 TB/s, a copy's rate).
 template <typename XT>
 __global__ void __launch_bounds__(kThreads)
 swiglu_keep8_kernel(const XT* __restrict__ g, const XT* __restrict__ u, int64_t ld, const int32_t* __restrict__ n_rows,
@@ -195,7 +200,8 @@ __device__ __forceinline__ float swiglu_bwd8_step(const Bwd8& a, const DT* dh, O
   return dot;
 }
 
-// Rows without weight gradients: steps of 8 columns, any row to any lane.
+// Rows without weight gradients: steps of 8 columns, any row to any lane (16384 x 1536,
+// float32 dh, bf16 out: 56 us, 303 MB at 5.4 TB/s).
 template <typename DT, typename OT>
 __global__ void __launch_bounds__(kThreads)
 swiglu_bwd8_kernel(Bwd8 a, RowMap m, const DT* __restrict__ dh, OT* __restrict__ dg, OT* __restrict__ du,
@@ -206,38 +212,41 @@ swiglu_bwd8_kernel(Bwd8 a, RowMap m, const DT* __restrict__ dh, OT* __restrict__
   });
 }
 
-// Rows with weight gradients dw = <dh, h>: WPR wavefronts per row, whose lane sums are
-// added in a fixed order. Four of them for few rows, which leave most of the chip's
-// wavefronts free (bf16, us with one against four: 1 x 1536 5.4 and 3.4, 1024 x 1536 7.6
-// and 6.3, 64 x 14336 35 and 11); one for many, without the join (4096 x 1536 14.2 and
-// 15.3, 32768 x 1536 96 and 106).
+// Rows with weight gradients dw = <dh, h>, TPR threads per row whose sums are added in a
+// fixed order. A wavefront (64) for most; four of them (256) for few long rows, which
+// leave most of the chip's wavefronts free (bf16, us with one against four: 1 x 1536 5.4
+// and 3.4, 1024 x 1536 7.6 and 6.3, 64 x 14336 35 and 11; but 4096 x 1536 14.2 and 15.3,
+// 32768 x 1536 96 and 106); for rows shorter than a wavefront's 512 columns (TPR 0) tpr
+// lanes, the least power of two from 8 on that covers the row's steps (65536 x 64 51 and
+// 12 us, 65536 x 256 63 and 38).
 constexpr int64_t kFewRows = 2048;
-template <typename DT, typename OT, int WPR>
+template <typename DT, typename OT, int TPR>
 __global__ void __launch_bounds__(kThreads)
-swiglu_bwd8_row_kernel(Bwd8 a, const DT* __restrict__ dh, OT* __restrict__ dg, OT* __restrict__ du,
+swiglu_bwd8_row_kernel(Bwd8 a, int tpr, const DT* __restrict__ dh, OT* __restrict__ dg, OT* __restrict__ du,
                        OT* __restrict__ h) {
-  constexpr int kWaves = kThreads / kWave, kRows = kWaves / WPR;  // rows per workgroup
+  constexpr int kWaves = kThreads / kWave;
   __shared__ float part[kWaves];
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x / kWave, sub = wave % WPR;
+  const int group = TPR ? TPR : tpr;  // threads per row, a power of two
+  const int rpw = kThreads / group;   // rows per workgroup
+  const int sub = threadIdx.x & (group - 1);
   const int64_t n = live_rows(a.n_rows, a.rows), nb = (a.F + 31) / 32;
-  for (int64_t row0 = (int64_t)blockIdx.x * kRows; row0 < n; row0 += (int64_t)gridDim.x * kRows) {
-    const int64_t row = row0 + wave / WPR;
+  for (int64_t row0 = (int64_t)blockIdx.x * rpw; row0 < n; row0 += (int64_t)gridDim.x * rpw) {
+    const int64_t row = row0 + threadIdx.x / group;
     float dot = 0.0f;
     if (row < n) {
       const float w = a.w_rows ? a.w_rows[row] : 1.0f;
-      for (int64_t col = (sub * kWave + lane) * kCols; col < a.F; col += WPR * kWave * kCols)
+      for (int64_t col = sub * kCols; col < a.F; col += group * kCols)
         dot += swiglu_bwd8_step(a, dh, dg, du, h, nb, row, col, w);
-#pragma unroll
-      for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
     }
-    if (WPR > 1) {
-      if (lane == 0) part[wave] = dot;
+    for (int o = min(group, kWave) / 2; o > 0; o >>= 1) dot += __shfl_xor(dot, o, kWave);
+    if (TPR > kWave) {
+      if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = dot;
       __syncthreads();
       if (sub == 0)
-        for (int i = 1; i < WPR; ++i) dot += part[wave + i];
+        for (int i = 1; i < kWaves; ++i) dot += part[i];
       __syncthreads();
     }
-    if (row < n && sub == 0 && lane == 0) {
+    if (row < n && sub == 0) {
       const int64_t to = a.row_slot ? a.row_slot[row] : row;
       if (to >= 0 && to < a.n_slots) a.dw[to] = dot;
     }
@@ -306,12 +315,14 @@ hipError_t launch_swiglu_bwd8(const SwigluBwd8Args& a, hipStream_t s) {
       const DT* dh = static_cast<const DT*>(a.dh);
       OT *dg = static_cast<OT*>(a.dg), *du = static_cast<OT*>(a.du), *h = static_cast<OT*>(a.h);
       if (a.dw) {
-        if (a.rows <= kFewRows && a.F > kWave * kCols) {
-          swiglu_bwd8_row_kernel<DT, OT, 4><<<(unsigned)a.rows, kThreads, 0, s>>>(b, dh, dg, du, h);
-        } else {
-          const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + 3) / 4, 1 << 20);
-          swiglu_bwd8_row_kernel<DT, OT, 1><<<blocks, kThreads, 0, s>>>(b, dh, dg, du, h);
-        }
+        int tpr = 8;
+        while (tpr < kWave && tpr * kCols < a.F) tpr *= 2;
+        if (a.F > kWave * kCols && a.rows <= kFewRows) tpr = kThreads;
+        const int rpw = kThreads / tpr;
+        const unsigned blocks = (unsigned)std::min<int64_t>((a.rows + rpw - 1) / rpw, 1 << 20);
+        if (tpr == kThreads) swiglu_bwd8_row_kernel<DT, OT, kThreads><<<blocks, kThreads, 0, s>>>(b, tpr, dh, dg, du, h);
+        else if (tpr == kWave) swiglu_bwd8_row_kernel<DT, OT, kWave><<<blocks, kThreads, 0, s>>>(b, tpr, dh, dg, du, h);
+        else swiglu_bwd8_row_kernel<DT, OT, 0><<<blocks, kThreads, 0, s>>>(b, tpr, dh, dg, du, h);
       } else {
         swiglu_bwd8_kernel<DT, OT><<<grid_of(a.rows, m), kThreads, 0, s>>>(b, m, dh, dg, du, h);
       }
