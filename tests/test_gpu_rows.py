@@ -184,7 +184,9 @@ def test_slots_outside_the_rows():
 
 
 ACTS = [(1, 8, "f32"), (3, 24, "bf16"), (7, 32, "f16"), (5, 40, "bf16"), (64, 136, "f32"), (33, 1032, "f16"),
-        (257, 776, "bf16"), (2, 8200, "bf16"), (1000, 72, "f32")]
+        (257, 776, "bf16"), (2, 8200, "bf16"), (1000, 72, "f32"),
+        # 16 columns per lane, rows that end inside a block
+        (1100, 1008, "bf16"), (700, 1552, "f16")]
 
 
 def act_values(rng, rows, cols, dtype):
@@ -269,10 +271,10 @@ def _within(got, ref, tol, what):
 SWIGLU = [(400, 64, "bf16", "f32", "bf16", True), (90, 256, "f32", "f32", "f32", True), (50, 512, "bf16", "bf16", "bf16", True),
           (1, 8, "bf16", "bf16", "bf16", False), (5, 40, "f32", "f32", "f32", True),
           (33, 136, "f16", "f16", "f16", True), (130, 776, "bf16", "f32", "bf16", True),
-          (64, 1536, "bf16", "bf16", "bf16", False), (7, 4104, "f32", "bf16", "f32", True),
+          (64, 1544, "bf16", "bf16", "bf16", False), (7, 4104, "f32", "bf16", "f32", True),
           (300, 264, "f16", "f32", "bf16", False),
           # many rows take one wavefront each, few long ones four
-          (2100, 528, "bf16", "bf16", "bf16", True), (3, 2056, "f16", "f32", "f32", True)]
+          (2100, 528, "bf16", "bf16", "bf16", True), (1200, 912, "f16", "f16", "f16", False), (3, 2056, "f16", "f32", "f32", True)]
 
 
 @pytest.mark.parametrize("rows,F,act,dht,out,weighted", SWIGLU)

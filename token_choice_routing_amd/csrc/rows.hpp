@@ -10,6 +10,14 @@ namespace moe {
 typedef _Float16 half_t;
 typedef half_t f16x4_t __attribute__((ext_vector_type(4)));
 
+// Two float32 values as bf16, rounded to nearest even by gfx950's v_cvt_pk_bf16_f32 (NaN
+// stays NaN, subnormals are kept).
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
+}
+
 // E = 4 or 8 elements at p (16-byte aligned rows, E-element aligned columns).
 template <int E>
 __device__ __forceinline__ void load_row(const float* p, float* v) {
@@ -60,10 +68,10 @@ __device__ __forceinline__ void store_row(float* p, const float* v) {
 template <int E>
 __device__ __forceinline__ void store_row(bf16_t* p, const float* v) {
   if constexpr (E == 8)
-    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
-                                             pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                             cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
   else
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
 }
 template <int E>
 __device__ __forceinline__ void store_row(half_t* p, const float* v) {
