@@ -785,16 +785,34 @@ __device__ __forceinline__ void combine_epilogue(const GemmProblem& pr, int m0, 
   }
 }
 
+// v_permlane32_swap_b32: lane half 0 gets (a, a of the lane 32 on), half 1 (b of the lane 32
+// back, b).
+__device__ __forceinline__ u32x2_t swap_halves(uint32_t a, uint32_t b) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  return u32x2_t{r[0], r[1]};
+#else
+  return u32x2_t{a, b};
+#endif
+}
+
 // The gate/up epilogue that keeps its pre-activations in 8 bits (kSwiGLUKeep8). The
 // wavefront holds rows rbase + 32 g + l32 and in each row 32 columns from c0, one block of
 // the checkpoint: lane half h has columns 8 q + 4 h + j, so a block's largest magnitude is
-// that of two lanes, 32 apart. Their code words change places pairwise (q 0 with q 2, q 1
-// with q 3), after which each lane holds 16 neighbouring columns and stores them at once.
+// that of two lanes, 32 apart. Their words change places pairwise (q 0 with q 2, q 1 with
+// q 3), after which each lane holds 16 neighbouring columns of the codes and of h and
+// stores 16 bytes at a time. Per element it stores 2 bytes of h and 2.06 of checkpoint
+// where kSwiGLUKeep stores 8 (the layer's gate/up launch at 16384 tokens, d = 2048, d_ff =
+// 1536, a quarter of 8 slots real and a shared expert: 728 us against 845, 673 with nothing
+// kept; stores of 8 bytes of h and exchanges through LDS took 7 us more). (Scale bytes:
+// one masked store per matrix. A pointer chosen per lane made the compiler spill.)
 __device__ __forceinline__ void keep8_epilogue(const GemmProblem& pr, int m0, int rows_valid, int rbase, int c0,
                                                f32x16_t (&acc)[2][4]) {
   const int lane = opaque_v((int)threadIdx.x) & (kWave - 1), half = lane >> 5, l32 = lane & 31;
   const int Nout = pr.n_out;
   const int64_t nb = (Nout + 31) / 32;
+  const int col = c0 + 16 * half;  // this lane's columns after the exchange
+  const bool wide = (Nout & 15) == 0;
 #pragma unroll
   for (int g = 0; g < 4; ++g) {
     const int rl = rbase + g * 32 + l32;
@@ -806,40 +824,35 @@ __device__ __forceinline__ void keep8_epilogue(const GemmProblem& pr, int m0, in
       uint32_t amax = 0;
 #pragma unroll
       for (int j = 0; j < 16; ++j) amax = max(amax, act8_magnitude(v[j]));
-      amax = max(amax, (uint32_t)__shfl_xor((int)amax, 32, kWave));
-      const uint32_t scale = act8_scale(amax);
+      const u32x2_t both = swap_halves(amax, amax);
+      const uint32_t scale = act8_scale(max(both[0], both[1]));
       uint32_t q[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) q[i] = act8_encode(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3], scale);
-      u32x4_t w;  // columns 16 half .. 16 half + 15 of the block
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t other = (uint32_t)__shfl_xor((int)(half ? q[i] : q[i + 2]), 32, kWave);
-        w[2 * i] = half ? other : q[i];
-        w[2 * i + 1] = half ? q[i + 2] : other;
-      }
+      const u32x2_t w0 = swap_halves(q[0], q[2]), w1 = swap_halves(q[1], q[3]);
       uint8_t* codes = static_cast<uint8_t*>(s ? pr.keep_u : pr.keep_g) + row * Nout;
-      const int col = c0 + 16 * half;
-      if (on && (Nout & 15) == 0) {
-        if (col < Nout) *reinterpret_cast<u32x4_t*>(codes + col) = w;
+      if (on && wide) {
+        if (col < Nout) *reinterpret_cast<u32x4_t*>(codes + col) = u32x4_t{w0[0], w0[1], w1[0], w1[1]};
       } else if (on) {  // rows that start at multiples of 8 only
-        if (col < Nout) *reinterpret_cast<u32x2_t*>(codes + col) = u32x2_t{w[0], w[1]};
-        if (col + 8 < Nout) *reinterpret_cast<u32x2_t*>(codes + col + 8) = u32x2_t{w[2], w[3]};
+        if (col < Nout) *reinterpret_cast<u32x2_t*>(codes + col) = w0;
+        if (col + 8 < Nout) *reinterpret_cast<u32x2_t*>(codes + col + 8) = w1;
       }
       if (on && half == s && c0 < Nout)
         static_cast<uint8_t*>(s ? pr.keep_su : pr.keep_sg)[row * nb + c0 / 32] = (uint8_t)scale;
     }
-    if (!on) continue;
-    bf16_t* crow = static_cast<bf16_t*>(pr.out) + row * Nout;
+    u32x2_t hq[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      const int col = c0 + 8 * q + 4 * half;
-      if (col < Nout) {
-        float h[4];
+      float h[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[j] = silu(acc[0][g][4 * q + j]) * acc[1][g][4 * q + j];
-        *reinterpret_cast<u32x2_t*>(crow + col) = u32x2_t{pack_f16x2(h[0], h[1]), pack_f16x2(h[2], h[3])};
-      }
+      for (int j = 0; j < 4; ++j) h[j] = silu(acc[0][g][4 * q + j]) * acc[1][g][4 * q + j];
+      hq[q] = u32x2_t{pack_f16x2(h[0], h[1]), pack_f16x2(h[2], h[3])};
+    }
+    bf16_t* crow = static_cast<bf16_t*>(pr.out) + row * Nout;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const u32x2_t a = swap_halves(hq[q][0], hq[q + 2][0]), b = swap_halves(hq[q][1], hq[q + 2][1]);
+      if (on && col + 8 * q < Nout) *reinterpret_cast<u32x4_t*>(crow + col + 8 * q) = u32x4_t{a[0], b[0], a[1], b[1]};
     }
   }
 }
