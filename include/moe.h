@@ -289,7 +289,7 @@ moe_status moe_combine_rows(const moe_dims* dims, int32_t rows_dtype, const void
  * required for those two). Other slots outside [0, T*min(K,N)) get dtopk_w = 0.
  *   dnull: MOE_NULL_COPY [T][d] float32, (sum of the token's null weights) dy_t, 0 for a
  *   token without null slots; MOE_NULL_CONSTANT [d] float32, the sum of those over all
- *   tokens (float32 sums of 64 tokens, joined in float64 in a fixed order);
+ *   tokens (float32 sums of 16 tokens, joined in float64 in a fixed order);
  *   ignored with MOE_NULL_ZERO.
  * The shared expert's gradient is dy itself. Every output may be NULL (not computed).
  * y_perm may be NULL when the expert outputs were not kept: dtopk_w of the real slots

@@ -118,21 +118,23 @@ __device__ __forceinline__ float wave_sum(float v) {
 
 // Gradient of the constant null expert's vector, sum over tokens of (sum of the null
 // slots' weights) dy_t: float32 sums over chunks of tokens, one wavefront per chunk and
-// 256 columns, then a float64 sum of the chunks in a fixed order. Short chunks for few
-// tokens keep the chip busy, longer ones for many keep the partial sums small next to dy.
+// 256 columns, then a float64 sum of the chunks in a fixed order. Chunks of 16 tokens (the
+// whole gradient in us, 8 slots a quarter real, with 8, 16 and 64: 200 x 1024 6.2, 6.5 and 10.7;
+// 2047 x 1024 10.3, 10.8 and 16.2; 16384 x 2048 91, 84 and 85: shorter ones write more
+// partial sums, longer ones leave few wavefronts with long chains).
 constexpr int kNullCols = 4;
-constexpr int null_chunk(int64_t T) { return T <= 4096 ? 16 : 64; }
+constexpr int kNullChunk = 16;
 // The units (chunk, columns) of wavefront `wave` of nwaves.
 template <typename ET>
 __device__ __forceinline__ void null_vector_partial(const ET* __restrict__ dy, const int32_t* __restrict__ slot_pos,
                                                     const float* __restrict__ topk_w, int64_t T, int K, int d,
                                                     int64_t wave, int64_t nwaves, float* __restrict__ part) {
-  const int lane = threadIdx.x & (kWave - 1), chunk = null_chunk(T);
+  const int lane = threadIdx.x & (kWave - 1);
   const int spans = (d + kWave * kNullCols - 1) / (kWave * kNullCols);
-  const int64_t chunks = (T + chunk - 1) / chunk;
+  const int64_t chunks = (T + kNullChunk - 1) / kNullChunk;
   for (int64_t unit = wave; unit < chunks * spans; unit += nwaves) {
-    const int64_t at = unit / spans, t0 = at * chunk;
-    const int n = (int)min<int64_t>(chunk, T - t0);
+    const int64_t at = unit / spans, t0 = at * kNullChunk;
+    const int n = (int)min<int64_t>(kNullChunk, T - t0);
     const int c = (int)(unit - at * spans) * kWave * kNullCols + lane * kNullCols;
     float my_w = 0.0f;  // lane i: token t0 + i
     bool any = false;
@@ -336,8 +338,7 @@ hipError_t launch_permute_bwd(const SlotSumArgs& a, hipStream_t stream) {
 }
 
 size_t combine_bwd_ws_bytes(int64_t T, int d, int null_kind) {
-  const int64_t chunk = null_chunk(T);
-  return null_kind == MOE_NULL_CONSTANT ? (size_t)((T + chunk - 1) / chunk) * d * sizeof(float) : 0;
+  return null_kind == MOE_NULL_CONSTANT ? (size_t)((T + kNullChunk - 1) / kNullChunk) * d * sizeof(float) : 0;
 }
 
 hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
@@ -347,8 +348,7 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
     typedef std::remove_pointer_t<decltype(e)> ET;
     float* dnull = a.null_stride ? a.dnull : nullptr;  // per token (copy)
     const bool vector = a.dnull && !a.null_stride;     // one vector (constant)
-    const int chunk = null_chunk(a.T);
-    const int64_t chunks = (a.T + chunk - 1) / chunk;
+    const int64_t chunks = (a.T + kNullChunk - 1) / kNullChunk;
     const int spans = (a.d + kWave * kNullCols - 1) / (kWave * kNullCols);
     const unsigned extra = vector ? (unsigned)std::min<int64_t>((chunks * spans + 3) / 4, 1 << 20) : 0;
     auto go = [&](auto wpt) {
@@ -359,6 +359,9 @@ hipError_t launch_combine_bwd(const CombineBwdArgs& a, hipStream_t stream) {
           static_cast<const ET*>(a.null_src), a.null_stride, static_cast<RT*>(a.dy_perm), a.w_perm, a.row_slot,
           a.dtopk_w, dnull, a.T, a.K, a.d, a.max_rows, blocks, a.part);
     };
+    // wavefronts per token by the spans of a row (bf16, 8 slots a quarter real, us with one,
+    // two and four: 16384 x 512 16.4, 19.9 and 28.6; x 1024 37.1, 36.4 and 46.5; x 2048
+    // 75.4, 69.9 and 66.7; 1000 x 4096 18.6, 11.8 and 9.5)
     if (a.d <= kSpan) go(std::integral_constant<int, 1>{});
     else if (a.d <= 2 * kSpan) go(std::integral_constant<int, 2>{});
     else go(std::integral_constant<int, 4>{});
