@@ -10,6 +10,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/csrc/utils/object_ptr.h>
 
 namespace {
 
@@ -38,7 +39,7 @@ PyObject* dense(PyObject*, PyObject* const* args, Py_ssize_t n) {
   const long dev = PyLong_AsLong(args[0]);
   if (PyErr_Occurred()) return nullptr;
   const Py_ssize_t m = (n - 1) / 3;
-  PyObject* out = PyTuple_New(m);
+  THPObjectPtr out(PyTuple_New(m));
   if (!out) return nullptr;
   for (Py_ssize_t i = 0; i < m; ++i) {
     PyObject* o = args[1 + 3 * i];
@@ -50,13 +51,10 @@ PyObject* dense(PyObject*, PyObject* const* args, Py_ssize_t n) {
       const at::Tensor& t = THPVariable_Unpack(o);
       if (same(t, dev, args[2 + 3 * i], args[3 + 3 * i]) && t.is_contiguous()) p = address(t);
     }
-    if (!p) {
-      Py_DECREF(out);
-      return PyErr_Occurred() ? nullptr : PyLong_FromSsize_t(i);
-    }
-    PyTuple_SET_ITEM(out, i, p);
+    if (!p) return PyErr_Occurred() ? nullptr : PyLong_FromSsize_t(i);
+    PyTuple_SET_ITEM(out.get(), i, p);
   }
-  return out;
+  return out.release();
   END_HANDLE_TH_ERRORS
 }
 
