@@ -34,6 +34,10 @@ __device__ __forceinline__ int64_t live_rows(const int32_t* n_rows, int64_t rows
   return n_rows ? min<int64_t>(max<int64_t>(n_rows[0], 0), rows) : rows;
 }
 
+// Scale bytes of a row (64 bits: cols may be any int32 multiple of 8, so cols + 31 is more
+// than an int holds for the last of them).
+__host__ __device__ __forceinline__ int64_t blocks_of(int cols) { return ((int64_t)cols + 31) / 32; }
+
 // Largest of a value over the lanes of a block (two or four, inside a quad).
 template <int C>
 __device__ __forceinline__ uint32_t block_max(uint32_t v) {
@@ -115,7 +119,7 @@ template <typename XT, int C>
 __global__ void __launch_bounds__(kThreads)
 act8_pack_kernel(const XT* __restrict__ x, int64_t ldx, const int32_t* __restrict__ n_rows, int64_t rows, int cols,
                  RowMap m, uint8_t* __restrict__ codes, uint8_t* __restrict__ scales) {
-  const int64_t nb = (cols + 31) / 32;
+  const int64_t nb = blocks_of(cols);
   for_steps<C>(m, live_rows(n_rows, rows), [&](int64_t row, int64_t col, bool on) {
     float v[C] = {};
     if (on) load_cols<C>(x + row * ldx + col, v);
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(kThreads)
 act8_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ scales,
                    const int32_t* __restrict__ n_rows, int64_t rows, int cols, RowMap m, XT* __restrict__ out,
                    int64_t ldo) {
-  const int64_t nb = (cols + 31) / 32;
+  const int64_t nb = blocks_of(cols);
   for_steps<C>(m, live_rows(n_rows, rows), [&](int64_t row, int64_t col, bool on) {
     if (!on) return;
     float v[C];
@@ -156,7 +160,7 @@ __global__ void __launch_bounds__(kThreads)
 swiglu_keep8_kernel(const XT* __restrict__ g, const XT* __restrict__ u, int64_t ld, const int32_t* __restrict__ n_rows,
                     int64_t rows, int F, RowMap m, XT* __restrict__ h, uint8_t* __restrict__ cg,
                     uint8_t* __restrict__ sg, uint8_t* __restrict__ cu, uint8_t* __restrict__ su) {
-  const int64_t nb = (F + 31) / 32;
+  const int64_t nb = blocks_of(F);
   for_steps<C>(m, live_rows(n_rows, rows), [&](int64_t row, int64_t col, bool on) {
     float z[C] = {}, v[C] = {};
     if (on) {
@@ -219,7 +223,7 @@ template <typename DT, typename OT, int C>
 __global__ void __launch_bounds__(kThreads)
 swiglu_bwd8_kernel(Bwd8 a, RowMap m, const DT* __restrict__ dh, OT* __restrict__ dg, OT* __restrict__ du,
                    OT* __restrict__ h) {
-  const int64_t nb = (a.F + 31) / 32;
+  const int64_t nb = blocks_of(a.F);
   for_steps<C>(m, live_rows(a.n_rows, a.rows), [&](int64_t row, int64_t col, bool on) {
     if (on) swiglu_bwd8_step<C>(a, dh, dg, du, h, nb, row, col, a.w_rows ? a.w_rows[row] : 1.0f);
   });
@@ -242,7 +246,7 @@ swiglu_bwd8_row_kernel(Bwd8 a, int tpr, const DT* __restrict__ dh, OT* __restric
   const int group = TPR ? TPR : tpr;  // threads per row, a power of two
   const int rpw = kThreads / group;   // rows per workgroup
   const int sub = threadIdx.x & (group - 1);
-  const int64_t n = live_rows(a.n_rows, a.rows), nb = (a.F + 31) / 32;
+  const int64_t n = live_rows(a.n_rows, a.rows), nb = blocks_of(a.F);
   for (int64_t row0 = (int64_t)blockIdx.x * rpw; row0 < n; row0 += (int64_t)gridDim.x * rpw) {
     const int64_t row = row0 + threadIdx.x / group;
     float dot = 0.0f;
