@@ -35,6 +35,7 @@ class MoeLayer:
         """weights_from: another MoeLayer whose device weights are reused (same arrays)."""
         cfg = workload.cfg
         self.cfg = cfg
+        self.kept = set()  # buffers that hold a forward's state
         self.T = cfg.T if T is None else T
         self.dims = dims_from_config(cfg, self.T)
         self.bf16 = self.dims.dtype == MOE_BF16
@@ -97,6 +98,7 @@ class MoeLayer:
     def _buffer(self, name, which):
         """A byte buffer of the size the library names, allocated on first use."""
         if getattr(self, name, None) is None:
+            self.kept.discard(name)
             setattr(self, name, torch.empty((max(workspace_bytes(self.dims, which), 256),), dtype=torch.uint8,
                                             device=self.x.device))
         return getattr(self, name)
@@ -104,6 +106,20 @@ class MoeLayer:
     def _backward_buffers(self):
         self._gradient_buffers()
         self._buffer("ws_bwd", MOE_WS_BACKWARD)
+
+    # The backwards that start from kept state read row counts and positions from it, so
+    # one without a forward before it would follow whatever its buffer holds: the forward
+    # names its buffer here when it is enqueued, and its backward asks. (A forward captured
+    # in a graph fills the buffer when the graph is replayed.)
+    def _keeping(self, name, forward, *args, **kw):
+        self.kept.discard(name)
+        forward(*args, **kw)
+        self.kept.add(name)
+
+    def _kept(self, name, forward):
+        if name not in self.kept or getattr(self, name, None) is None:
+            raise RuntimeError(f"no state of a forward: {forward}() has to come before its backward")
+        return getattr(self, name)
 
     def backward(self, dy, alpha=0.0, beta=0.0, stream=None):
         """Gradients of <dy, y> + alpha L_bal + beta L_z (float32 device tensors,
@@ -117,30 +133,33 @@ class MoeLayer:
         """The forward that keeps its routing and pre-activations in the backward's
         workspace (counts, P and scalars are written too; the routing outputs are not)."""
         self._backward_buffers()
-        moe_layer_forward_train(self.dims, self.params, self.y, self.aux_train, self.ws_bwd, stream=stream)
+        self._keeping("ws_bwd", moe_layer_forward_train, self.dims, self.params, self.y, self.aux_train, self.ws_bwd,
+                      stream=stream)
         return self.y
 
     def backward_saved(self, dy, alpha=0.0, beta=0.0, stream=None):
-        """backward() from the state of the last forward_train() call."""
-        self._backward_buffers()
-        moe_layer_backward_saved(self.dims, self.params, dy, alpha, beta, self.grads_struct, self.ws_bwd,
-                                 stream=stream)
+        """backward() from the state of the last forward_train() call (RuntimeError if
+        there was none)."""
+        ws = self._kept("ws_bwd", "forward_train")
+        self._gradient_buffers()
+        moe_layer_backward_saved(self.dims, self.params, dy, alpha, beta, self.grads_struct, ws, stream=stream)
         return self.grads
 
     def forward_train8(self, ws=None, stream=None):
         """forward_train() whose state is kept in 8 bits in self.state8; ws: scratch of
         MOE_WS_TRAIN8 bytes, which layers of a model can share (its own by default)."""
         self._gradient_buffers()
-        moe_layer_forward_train8(self.dims, self.params, self.y, self.aux_train,
-                                 self._buffer("state8", MOE_WS_STATE8),
-                                 self._buffer("ws_train8", MOE_WS_TRAIN8) if ws is None else ws, stream=stream)
+        self._keeping("state8", moe_layer_forward_train8, self.dims, self.params, self.y, self.aux_train,
+                      self._buffer("state8", MOE_WS_STATE8),
+                      self._buffer("ws_train8", MOE_WS_TRAIN8) if ws is None else ws, stream=stream)
         return self.y
 
     def backward_saved8(self, dy, alpha=0.0, beta=0.0, ws=None, stream=None):
-        """backward() from the state of the last forward_train8() call."""
+        """backward() from the state of the last forward_train8() call (RuntimeError if
+        there was none)."""
+        state = self._kept("state8", "forward_train8")
         self._gradient_buffers()
-        moe_layer_backward_saved8(self.dims, self.params, dy, alpha, beta, self.grads_struct,
-                                  self._buffer("state8", MOE_WS_STATE8),
+        moe_layer_backward_saved8(self.dims, self.params, dy, alpha, beta, self.grads_struct, state,
                                   self._buffer("ws_train8", MOE_WS_TRAIN8) if ws is None else ws, stream=stream)
         return self.grads
 
