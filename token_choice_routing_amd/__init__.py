@@ -173,7 +173,12 @@ def _row_stream(stream, dev):
     """The stream of a call on device dev (torch's current one by default)."""
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
-    return stream if isinstance(stream, int) else stream.cuda_stream
+    if isinstance(stream, int):
+        return stream
+    if getattr(stream, "device_index", dev) != dev:
+        raise ValueError(f"stream: expected one of the current device (cuda:{dev}), got one of "
+                         f"cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 def _refuse(name, t, dev, dtype, shape, layout="a contiguous tensor"):
