@@ -61,17 +61,16 @@ class LayerGrads(ctypes.Structure):
 
 
 _lib = None
-_marshal = None  # argument checks of the row operators (csrc/marshal.cpp), loaded with the library
+_marshal = None  # argument checks of the row operators (csrc/marshal.cpp), loaded on their first call
 _P = ctypes.c_void_p
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
-    global _lib, _marshal
+    global _lib
     if _lib is not None:
         return _lib
-    if not os.path.exists(path) or not os.path.exists(MARSHAL_PATH):
+    if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run `python -m token_choice_routing_amd.build`")
-    _marshal = importlib.import_module("._marshal", __name__)
     lib = ctypes.CDLL(path)
     D, I, L = ctypes.POINTER(Dims), ctypes.c_int32, ctypes.c_int64
     sig = {
@@ -164,6 +163,20 @@ _DTYPES = {v: k for k, v in _ROW_TYPES.items()}
 # sees addresses only, so a tensor of another type or shape or on another device than the
 # current one is refused here.
 
+def _load_marshal():
+    """The native checks. Only these calls need them: the layer's run without."""
+    global _marshal
+    if _marshal is None:
+        build = "run `python -m token_choice_routing_amd.build`"
+        if not os.path.exists(MARSHAL_PATH):
+            raise ImportError(f"{MARSHAL_PATH} (argument checks of the row operators) is not built; {build}")
+        try:
+            _marshal = importlib.import_module("._marshal", __name__)
+        except ImportError as e:
+            raise ImportError(f"{MARSHAL_PATH} does not load with this torch, {build}: {e}") from e
+    return _marshal
+
+
 def _device():
     """Index of the current device; tensors of these calls have to be on it."""
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
@@ -196,7 +209,7 @@ def _refuse(name, t, dev, dtype, shape, layout="a contiguous tensor"):
 def _dense(dev, names, *spec):
     """Device addresses of dense tensors; spec: a tensor (or None), its type and its shape
     for each name."""
-    got = _marshal.dense(dev, *spec)
+    got = (_marshal or _load_marshal()).dense(dev, *spec)
     if got.__class__ is int:
         _refuse(names[got], spec[3 * got], dev, spec[3 * got + 1], spec[3 * got + 2])
     return got
@@ -205,7 +218,7 @@ def _dense(dev, names, *spec):
 def _matrix(name, t, dev, dtype, shape):
     """(device address, elements from row to row) of a [rows][cols] tensor whose rows may
     be spaced (a column range of a wider matrix) but are dense inside."""
-    got = _marshal.matrix(dev, t, dtype, shape)
+    got = (_marshal or _load_marshal()).matrix(dev, t, dtype, shape)
     if got is None:
         _refuse(name, t, dev, dtype, shape, "rows that are dense and do not overlap")
     return got

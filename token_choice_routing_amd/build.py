@@ -4,7 +4,9 @@
     python -m token_choice_routing_amd.build
 
 Every call compiles all sources (one hipcc process per file, in parallel) and
-links the shared libraries next to this file.
+links the shared libraries next to this file. Without a C++ compiler or torch's
+headers the HIP library is built all the same, with a warning: the binding's row
+operators then refuse to run, the others do not need the checks.
 """
 import os
 import subprocess
@@ -49,6 +51,27 @@ def _marshal_cmd(out):
             "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
 
 
+def _compile_marshal(out) -> str:
+    """Compiles the argument checks; returns what went wrong ("" if nothing did)."""
+    try:
+        rc, text = _run(_marshal_cmd(out))
+    except OSError as e:  # no such compiler
+        rc, text = 1, str(e)
+    return (text or f"g++ status {rc}") if rc else ""
+
+
+def _install_marshal(new, problem):
+    """Puts the compiled checks in place. If they did not compile, those of an earlier build
+    do not stay either: they may not match the sources or torch."""
+    if not problem:
+        os.replace(new, MARSHAL)
+        return
+    if os.path.exists(MARSHAL):
+        os.remove(MARSHAL)
+    print(f"warning: {MARSHAL} is not built, the Python binding's row operators will refuse to run:\n{problem}",
+          file=sys.stderr)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     objs, cmds = [], []
@@ -56,8 +79,8 @@ def build(verbose: bool = False) -> str:
         obj = os.path.join(BUILD, src.replace(".hip", ".o"))
         objs.append(obj)
         cmds.append([HIPCC, *FLAGS, "-c", os.path.join(CSRC, src), "-o", obj])
-    cmds.append(_marshal_cmd(MARSHAL + ".tmp"))
     with ThreadPoolExecutor(max_workers=min(len(cmds), os.cpu_count() or 4, 8)) as ex:
+        marshal = ex.submit(_compile_marshal, MARSHAL + ".tmp")
         results = list(ex.map(_run, cmds))
     for cmd, (rc, out) in zip(cmds, results):
         if out.strip() and (verbose or rc):
@@ -70,7 +93,7 @@ def build(verbose: bool = False) -> str:
         print(out, file=sys.stderr)
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
-    os.replace(MARSHAL + ".tmp", MARSHAL)
+    _install_marshal(MARSHAL + ".tmp", marshal.result())
     return LIB
 
 
