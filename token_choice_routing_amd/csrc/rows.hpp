@@ -8,7 +8,6 @@
 namespace moe {
 
 typedef _Float16 half_t;
-typedef half_t f16x4_t __attribute__((ext_vector_type(4)));
 
 // Two float32 values as bf16, rounded to nearest even by gfx950's v_cvt_pk_bf16_f32 (NaN
 // stays NaN, subnormals are kept).
@@ -18,7 +17,8 @@ __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2_t{lo, hi}), bf16x2_t));
 }
 
-// E = 4 or 8 elements at p (16-byte aligned rows, E-element aligned columns).
+// E elements at p (16-byte aligned rows, E-element aligned columns): 8 of any type, or 4
+// float32 ones.
 template <int E>
 __device__ __forceinline__ void load_row(const float* p, float* v) {
 #pragma unroll
@@ -30,33 +30,20 @@ __device__ __forceinline__ void load_row(const float* p, float* v) {
 }
 template <int E>
 __device__ __forceinline__ void load_row(const bf16_t* p, float* v) {
-  if constexpr (E == 8) {
-    const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p);
+  static_assert(E == 8);
+  const u32x4_t a = *reinterpret_cast<const u32x4_t*>(p);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[2 * j] = __uint_as_float(a[j] << 16);
-      v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
-    }
-  } else {
-    const u32x2_t a = *reinterpret_cast<const u32x2_t*>(p);
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      v[2 * j] = __uint_as_float(a[j] << 16);
-      v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
-    }
+  for (int j = 0; j < 4; ++j) {
+    v[2 * j] = __uint_as_float(a[j] << 16);
+    v[2 * j + 1] = __uint_as_float(a[j] & 0xffff0000u);
   }
 }
 template <int E>
 __device__ __forceinline__ void load_row(const half_t* p, float* v) {
-  if constexpr (E == 8) {
-    const f16x8_t a = *reinterpret_cast<const f16x8_t*>(p);
+  static_assert(E == 8);
+  const f16x8_t a = *reinterpret_cast<const f16x8_t*>(p);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
-  } else {
-    const f16x4_t a = *reinterpret_cast<const f16x4_t*>(p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = (float)a[j];
-  }
+  for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
 }
 
 template <int E>
@@ -67,19 +54,15 @@ __device__ __forceinline__ void store_row(float* p, const float* v) {
 }
 template <int E>
 __device__ __forceinline__ void store_row(bf16_t* p, const float* v) {
-  if constexpr (E == 8)
-    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
-                                             cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
-  else
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
+  static_assert(E == 8);
+  *reinterpret_cast<u32x4_t*>(p) = u32x4_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]),
+                                           cvt_bf16x2(v[4], v[5]), cvt_bf16x2(v[6], v[7])};
 }
 template <int E>
 __device__ __forceinline__ void store_row(half_t* p, const float* v) {
-  if constexpr (E == 8)
-    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]),
-                                             pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7])};
-  else
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+  static_assert(E == 8);
+  *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3]),
+                                           pack_f16x2(v[4], v[5]), pack_f16x2(v[6], v[7])};
 }
 
 // E consecutive elements as loaded, converted where they are used: a load whose result
