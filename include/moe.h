@@ -290,7 +290,8 @@ moe_status moe_combine_rows(const moe_dims* dims, int32_t rows_dtype, const void
  *   dnull: MOE_NULL_COPY [T][d] float32, (sum of the token's null weights) dy_t, 0 for a
  *   token without null slots; MOE_NULL_CONSTANT [d] float32, the sum of those over all
  *   tokens (float32 sums of 16 tokens, joined in float64 in a fixed order);
- *   ignored with MOE_NULL_ZERO.
+ *   ignored with MOE_NULL_ZERO. T = 0 writes nothing here either: this vector, a sum over
+ *   no tokens then, is the caller's to clear.
  * The shared expert's gradient is dy itself. Every output may be NULL (not computed).
  * y_perm may be NULL when the expert outputs were not kept: dtopk_w of the real slots
  * is then left unwritten (moe_swiglu_backward8 can supply it through row_slot). Rows of
@@ -330,9 +331,13 @@ moe_status moe_permute_backward(const moe_dims* dims, int32_t rows_dtype, const 
  * so |v - q 2^e| <= 2^(e-1), or 2^e where |v| > 127.5 2^e. Codes and values are exact
  * functions of the input. A block with a NaN or an infinity has scale byte 255 and
  * codes 0 and stands for NaN. The sign of a zero is lost.
+ * The layout is that of MXINT8 (OCP microscaling: blocks of 32, int8 elements, a power of
+ * two per block), but the byte here is that of one step of the codes; MXINT8's is that of
+ * 64 steps, larger by 6 for the same values.
  * Conventions of these entry points (no dims):
  *   - dtype arguments: MOE_F32, MOE_BF16 or MOE_F16. cols and d_ff are multiples of 8;
- *     rows >= 0, rows = 0 is a no-op; rows * cols < 2^40.
+ *     rows >= 0, rows = 0 is a no-op; ld and rows * ld below 2^40, else
+ *     MOE_ERR_UNSUPPORTED.
  *   - ld arguments: elements from one row to the next, a multiple of 8, at least cols
  *     (so gate and up may be the halves of one [rows][2 d_ff] matrix). Other tensors
  *     are dense.
@@ -371,7 +376,8 @@ moe_status moe_swiglu_keep8(int64_t rows, int32_t d_ff, int32_t dtype, const voi
  * With dh = dy W_down^T of the unweighted output gradient and w_rows, row_slot from
  * moe_combine_backward, dw is the routing weights' gradient, expert outputs not kept.
  * Sums in float32 in a fixed order; a row's sum runs over the checkpoint's h before its
- * rounding to out_dtype.
+ * rounding to out_dtype. With a 16-bit out_dtype s is off by up to (1.5 |z| + 6) 2^-23 of
+ * itself (float32: a few 2^-24), in dw's terms as well.
  */
 moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_g,
                                 const uint8_t* scales_g, const int8_t* codes_u,
@@ -489,16 +495,17 @@ moe_status moe_layer_backward(const moe_dims* dims, const moe_layer_params* para
  * moe_layer_forward_train computes y exactly as moe_layer_forward does (bit for bit)
  * and leaves in ws -- moe_workspace_bytes(dims, MOE_WS_BACKWARD) bytes, the backward's
  * workspace -- the routing (logits, selection, weights), the permutation, the pool
- * counts f and the expert pre-activations g, u (float32) and h = silu(g) u (bf16), routed
- * and shared. aux may ask for P, counts and scalars only (its other pointers must be
- * NULL: MOE_ERR_ARG; the routing outputs stay in ws). Same limits as moe_layer_backward
+ * counts f and the expert pre-activations g, u (IEEE half where the gate/up product runs
+ * on the 256 x 256 tiles, else float32) and h = silu(g) u (bf16), routed and shared. aux
+ * may ask for P, counts and scalars only (its other pointers must be NULL:
+ * MOE_ERR_ARG; the routing outputs stay in ws). Same limits as moe_layer_backward
  * (bf16, MOE_NULL_ZERO).
  * moe_layer_backward_saved then returns what moe_layer_backward returns for the same
  * inputs and dy (bit for bit), reading that state from ws instead of recomputing it: ws
  * must be the workspace of a moe_layer_forward_train call with the same dims, params
  * and x, with nothing written to it in between (not checked; the ws memory of the pair
  * is the caller's). Saves the recompute (routing, permutation and one gate/up GEMM);
- * the forward instead stores g and u (8 bytes per row and column) next to h.
+ * the forward instead stores g and u (4 or 8 bytes per row and column) next to h.
  * All enqueued on `stream`; no host synchronisation.
  */
 moe_status moe_layer_forward_train(const moe_dims* dims, const moe_layer_params* params, void* y,
@@ -513,7 +520,11 @@ moe_status moe_layer_backward_saved(const moe_dims* dims, const moe_layer_params
  * each and share one workspace. state: MOE_WS_STATE8 bytes, written by the forward and
  * read by the backward: routing, permutation, pool counts and the 8-bit checkpoints
  * (moe_act8_pack's format) of the pre-activations g and u, routed and shared: 2.06
- * bytes per row and column instead of the 4 (g, u) and 2 (h) of the other pair. ws:
+ * bytes per row and column instead of the 4 (g, u) and 2 (h) of the other pair. Where the
+ * gate/up product does not run on the 256 x 256 tiles (T*min(K,N)/N below 512, or T with a
+ * shared expert), the forward computes g and u a second time, in float32 next to h, and
+ * encodes them from ws: the state is as small, but time and scratch are those of the
+ * other pair or more. ws:
  * MOE_WS_TRAIN8 bytes, scratch of each call, free in between (calls that overlap need
  * their own).
  * The forward computes y exactly as moe_layer_forward does (bit for bit); aux as in

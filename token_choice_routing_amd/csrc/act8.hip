@@ -9,7 +9,9 @@
 // the code q (int8) stands for q 2^e, and the block's scale byte is e + 127: float32
 // exponent bits, so the scale and every product with it are exact and the codes do not
 // depend on how they are computed. |v - q 2^e| <= 2^(e-1), or 2^e where |v| > 127.5 2^e
-// is clamped; either is at most 2^-7 of the block's largest value (64 to 128 steps).
+// is clamped; either is at most 2^-7 of the block's largest value (64 to 128 steps) while
+// that is at least 2^-120. Below, where e stays -126, half a step is 2^-127: a block within
+// 2^-127 becomes zeros.
 // int8 steps are uniform, so a block's error goes by its largest value; an 8-bit float
 // (4 significant bits) would be off by up to 2^-4 of that value itself. A block that
 // holds a NaN or an infinity has scale byte 255 and codes 0 and stands for NaN.
@@ -144,9 +146,11 @@ act8_unpack_kernel(const uint8_t* __restrict__ codes, const uint8_t* __restrict_
   });
 }
 
-// 1 / (1 + e^-z). For 16-bit results the hardware's exponential and reciprocal (a few
-// 2^-22 relative, far below their half steps of 2^-9 and 2^-12); float32 results take
-// the full-precision functions.
+// 1 / (1 + e^-z). FAST: the hardware's exponential and reciprocal, for 16-bit h, dg and du.
+// The exponential's argument z log2 e is off by its own rounding, so the relative error
+// grows with |z|: at most (1.5 |z| + 6) 2^-23, 2^-16 at z = -80 (half a step of bf16 is
+// 2^-8, of half 2^-11). The backward's dw, a float32 sum, takes the sigmoid of the h it is
+// summed from, so with 16-bit outputs its terms carry that error too.
 template <bool FAST>
 __device__ __forceinline__ float sigmoid(float z) {
   if constexpr (FAST) return __builtin_amdgcn_rcpf(1.0f + __expf(-z));
@@ -235,7 +239,8 @@ swiglu_bwd8_kernel(Bwd8 a, RowMap m, const DT* __restrict__ dh, OT* __restrict__
 // and 3.4, 1024 x 1536 7.6 and 6.3, 64 x 14336 35 and 11; but 4096 x 1536 14.2 and 15.3,
 // 32768 x 1536 96 and 106); for rows shorter than a wavefront's 512 columns (TPR 0) tpr
 // lanes, the least power of two from 8 on that covers the row's steps (65536 x 64 51 and
-// 12 us, 65536 x 256 63 and 38).
+// 12 us, 65536 x 256 63 and 38). rows is the tensors' capacity, the only count the host
+// has: few live rows of a large capacity keep one wavefront each.
 constexpr int64_t kFewRows = 2048;
 template <typename DT, typename OT, int TPR, int C>
 __global__ void __launch_bounds__(kThreads)
@@ -287,6 +292,8 @@ unsigned grid_of(int64_t rows, const RowMap& m) {
 // 256 x 1536 2.5 and 2.7, with half the wavefronts; keep8 77 and 74, 7.5 and 7.2, 3.0 and
 // 3.4). Float32 gains nothing (24.6 and 24.5; keep8 65 and 70), and the decoding kernels,
 // whose stores are wide anyway, lose (unpack 30.3 and 32.3, SwiGLU backward 91 and 98).
+// rows is the capacity here too: few live rows of a large one take 16 columns, at the small
+// sizes' loss above.
 template <typename XT, typename F>
 hipError_t with_cols(int64_t rows, int cols, F&& f) {
   if constexpr (sizeof(XT) == 2)
