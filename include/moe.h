@@ -386,6 +386,80 @@ moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_
                                 int64_t n_slots, int32_t out_dtype, void* dg, void* du, int64_t ld,
                                 void* h, float* dw, moe_stream stream);
 
+/*
+ * Grouped products for experts of one's own (the grouped GEMM of the paper review's
+ * "implementation" paragraph as plain products, with their gradients). Rows are in expert
+ * order as moe_permute leaves them, group e owning segment e of `offsets`; the segment
+ * rules are those of moe_expert_ffn (clamped; NULL offsets with n_groups == 1 only; rows
+ * outside the segments are neither read nor written).
+ *   moe_grouped_mm        out[p] = W[e] a[src(p)]
+ *   moe_grouped_mm_dgrad  da[p] = W[e]^T dy[p]
+ *   moe_grouped_mm_wgrad  dW[e] = dw_add[e] + sum over segment e of dy[p] a[src(p)]^T
+ * src(p) = a_rows[p] clamped to [0, a_nrows) (perm_token of moe_permute: the gather fused
+ * in), or p when a_rows is NULL. A group without rows gets dW[e] = dw_add[e] (0 without
+ * one), also when rows = 0; the other two are no-ops then.
+ * The gather's own gradient (several rows of one token) is moe_permute_backward's.
+ *   a: [a_nrows or rows][lda], dy: [rows][ldy], w: [n_groups][n_out][k_dim], all dtype;
+ *   out: [rows][ldo], da: [rows][lda], dw: [n_groups][n_out][k_dim], of out_dtype;
+ *   dw_add: float32 [n_groups][n_out][k_dim] or NULL; dw may be dw_add itself (float32).
+ * dtype and out_dtype: MOE_F32, MOE_BF16 or MOE_F16. Sums in float32 (16-bit products are
+ * exact there) in an order fixed by the sizes, no atomics; one rounding to out_dtype.
+ * n_out and k_dim multiples of 8 up to MOE_MM_MAX_DIM, ld arguments (elements from one row
+ * to the next) multiples of 8 up to twice that, n_groups up to MOE_MAX_EXPERTS, rows below
+ * 2^31 - 512 and n_groups (rows / 64 + 1) (max(n_out, k_dim) / 64 + 1) below 2^31; with
+ * a_rows, (a_nrows + 1) rows of lda elements must fit in 4 GB; else MOE_ERR_UNSUPPORTED.
+ * No workspace. Outputs must not overlap inputs (except dw and dw_add) or each other.
+ */
+#define MOE_MM_MAX_DIM (1 << 20)
+moe_status moe_grouped_mm(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows, const void* a,
+                          int64_t lda, const int32_t* a_rows, int64_t a_nrows, const int32_t* offsets, const void* w,
+                          int32_t out_dtype, void* out, int64_t ldo, moe_stream stream);
+moe_status moe_grouped_mm_dgrad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
+                                const void* dy, int64_t ldy, const int32_t* offsets, const void* w, int32_t out_dtype,
+                                void* da, int64_t lda, moe_stream stream);
+moe_status moe_grouped_mm_wgrad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
+                                const void* dy, int64_t ldy, const void* a, int64_t lda, const int32_t* a_rows,
+                                int64_t a_nrows, const int32_t* offsets, const float* dw_add, int32_t out_dtype,
+                                void* dw, moe_stream stream);
+
+/*
+ * 4-bit expert weights for serving: a decode step reads each chosen expert's weights for a
+ * row or a few, so their bytes are its time. A matrix [rows][cols], cols a multiple of 32,
+ * is held as codes uint8 [rows][cols / 2] (even columns in the low half of a byte) and one
+ * scale byte per block of 32 columns, scales uint8 [rows][cols / 32]. With amax the largest
+ * magnitude in the block:
+ *   e = max(floor(log2 amax) - 2, -126);  scale byte = e + 127
+ *   code: sign bit and the index of the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 to |w| 2^-e,
+ *   ties to the even index, larger values to 6; the code stands for that value times 2^e.
+ * This is MXFP4 (OCP microscaling: blocks of 32, e2m1 elements, a power of two per block),
+ * and scale bytes of other origin are taken as it defines them (0 is 2^-127). A block with
+ * a NaN or an infinity has scale byte 255 and codes 0 and stands for NaN.
+ * |w - value| <= amax / 4 at the top of a block (between 6 and 8 steps), amax / 8 elsewhere.
+ * rows >= 0 (0 is a no-op), rows * cols below 2^40. No workspace.
+ */
+moe_status moe_weights4_pack(int64_t rows, int32_t cols, int32_t dtype, const void* w, uint8_t* codes, uint8_t* scales,
+                             moe_stream stream);
+/* The values 4-bit weights stand for, rounded to dtype (exact in MOE_F32 and MOE_BF16). */
+moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const uint8_t* codes, const uint8_t* scales,
+                               void* out, moe_stream stream);
+
+/*
+ * moe_grouped_gemm4 -- moe_grouped_gemm with 4-bit weights, for the rows of a decode step:
+ *   op = MOE_GEMM_GATE_UP: out[p] = silu(W0[e] a[src(p)]) * (W1[e] a[src(p)])
+ *   op = MOE_GEMM_DOWN:    out[p] = W0[e] a[src(p)]          (codes1, scales1 unused)
+ * W0 (and W1) are what codes [n_groups][n_out][k_dim / 2] and scales
+ * [n_groups][n_out][k_dim / 32] stand for; a, a_rows, offsets, out, the types and the limits
+ * are those of moe_grouped_mm, k_dim a multiple of 32. Products of the weights with a are
+ * exact, sums in float32. Any number of rows is taken, but every 16 rows of an expert read
+ * its weights again: from about 64 rows an expert, moe_weights4_unpack and moe_grouped_mm
+ * take less time. No workspace.
+ */
+moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
+                             const void* a, int64_t lda, const int32_t* a_rows, int64_t a_nrows,
+                             const int32_t* offsets, const uint8_t* codes0, const uint8_t* scales0,
+                             const uint8_t* codes1, const uint8_t* scales1, int32_t out_dtype, void* out, int64_t ldo,
+                             moe_stream stream);
+
 /* Device pointers of the layer's inputs. */
 typedef struct {
   const void* x;               /* [T][d_model] dtype */

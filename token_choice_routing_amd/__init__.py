@@ -89,6 +89,12 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_act8_unpack": [L, I, I, _P, _P, _P, _P, L, _P],
         "moe_swiglu_keep8": [L, I, I, _P, _P, L, _P, _P, _P, _P, _P, _P, _P],
         "moe_swiglu_backward8": [L, I, _P, _P, _P, _P, _P, I, _P, _P, _P, L, I, _P, _P, L, _P, _P, _P],
+        "moe_grouped_mm": [I, I, I, I, L, _P, L, _P, L, _P, _P, I, _P, L, _P],
+        "moe_grouped_mm_dgrad": [I, I, I, I, L, _P, L, _P, _P, I, _P, L, _P],
+        "moe_grouped_mm_wgrad": [I, I, I, I, L, _P, L, _P, L, _P, L, _P, _P, I, _P, _P],
+        "moe_grouped_gemm4": [I, I, I, I, I, L, _P, L, _P, L, _P, _P, _P, _P, _P, I, _P, L, _P],
+        "moe_weights4_pack": [L, I, I, _P, _P, _P, _P],
+        "moe_weights4_unpack": [L, I, I, _P, _P, _P, _P],
         "moe_aux_stats": [D, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P],
         "moe_layer_forward": [D, ctypes.POINTER(LayerParams), _P, ctypes.POINTER(AuxOut), _P,
                               ctypes.c_size_t, _P],
@@ -469,6 +475,134 @@ def moe_swiglu_backward8(g_codes, g_scales, u_codes, u_scales, dh, dg, du, h=Non
         n_rows, i32, _COUNT, dh, tdh, shape, w_rows, f32, col, row_slot, i32, col, h, dt, shape, dw, f32, dw_shape)
     _check(lib.moe_swiglu_backward8(rows, F, cg, sg, cu, su, pn, _ROW_TYPES[tdh], pd, pw, pr, n_slots, _ROW_TYPES[dt],
                                     pg, pu, ld, ph, pdw, _row_stream(stream, dev)), "moe_swiglu_backward8")
+
+
+W4_BLOCK = 32  # columns of 4-bit weights that share a scale byte
+
+
+def weights4_shapes(shape):
+    """(shape of the codes, shape of the scales), both uint8, of 4-bit weights [..., cols]."""
+    *lead, cols = shape
+    return (*lead, cols // 2), (*lead, cols // W4_BLOCK)
+
+
+def _weights(name, t):
+    """(type, shape) of expert weights [groups][n_out][k_dim]."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype not in _ROW_TYPES:
+        raise ValueError(f"{name}: expected [groups][n_out][k_dim] of float32, bfloat16 or float16")
+    return t.dtype, t.shape
+
+
+_ROWS_OF = ("offsets", "a_rows")
+
+
+def _grouped(dev, groups, rows, offsets, a_rows):
+    """Addresses of a grouped product's offsets (None: one group of all rows) and row numbers."""
+    return _dense(dev, _ROWS_OF, offsets, torch.int32, (groups + 1,), a_rows, torch.int32, (rows,))
+
+
+def _source(a, rows, a_rows, k):
+    """Shape that a grouped product's row operand has: [rows][k], or any number of rows
+    where a_rows names them."""
+    return (a.shape[0] if a_rows is not None and isinstance(a, torch.Tensor) and a.dim() == 2 else rows, k)
+
+
+def moe_grouped_mm(a, offsets, w, out, a_rows=None, stream=None):
+    """out[p] = W[e] a[p] (a[a_rows[p]] with a_rows) for the rows p of every expert e. a:
+    [rows or tokens][k], w: [experts][n][k] of one type; out: [rows][n] of float32, bfloat16
+    or float16. Rows of a and out may be spaced; offsets: int32 [experts + 1]."""
+    lib, dev = load_library(), _device()
+    (dt, (G, n, k)), (ot, shape) = _weights("w", w), _matrix_like("out", out)
+    rows = shape[0]
+    source = _source(a, rows, a_rows, k)
+    (pa, lda), (po, ldo) = _matrix("a", a, dev, dt, source), _matrix("out", out, dev, ot, (rows, n))
+    pf, pr = _grouped(dev, G, rows, offsets, a_rows)
+    pw, = _dense(dev, ("w",), w, dt, w.shape)
+    _check(lib.moe_grouped_mm(_ROW_TYPES[dt], G, n, k, rows, pa, lda, pr, source[0], pf, pw, _ROW_TYPES[ot], po, ldo,
+                              _row_stream(stream, dev)), "moe_grouped_mm")
+
+
+def moe_grouped_mm_dgrad(dy, offsets, w, da, stream=None):
+    """Data gradient of moe_grouped_mm: da[p] = W[e]^T dy[p]. dy: [rows][n] and w:
+    [experts][n][k] of one type; da: [rows][k] of any. (Of a gathered product this is the
+    gathered rows' gradient; moe_permute_backward brings it to the tokens.)"""
+    lib, dev = load_library(), _device()
+    (dt, (G, n, k)), (ot, shape) = _weights("w", w), _matrix_like("da", da)
+    rows = shape[0]
+    (pd, ldy), (po, ldo) = _matrix("dy", dy, dev, dt, (rows, n)), _matrix("da", da, dev, ot, (rows, k))
+    pf, _ = _grouped(dev, G, rows, offsets, None)
+    pw, = _dense(dev, ("w",), w, dt, w.shape)
+    _check(lib.moe_grouped_mm_dgrad(_ROW_TYPES[dt], G, n, k, rows, pd, ldy, pf, pw, _ROW_TYPES[ot], po, ldo,
+                                    _row_stream(stream, dev)), "moe_grouped_mm_dgrad")
+
+
+_WGRAD = ("dw_add", "dw")
+
+
+def moe_grouped_mm_wgrad(dy, a, offsets, dw, a_rows=None, dw_add=None, stream=None):
+    """Weight gradient of moe_grouped_mm: dw[e] = dw_add[e] + the sum of dy[p] a[p]^T over
+    the expert's rows (a[a_rows[p]] with a_rows). dy: [rows][n], a: [rows or tokens][k] of
+    one type; dw: [experts][n][k] of any; dw_add: float32 like dw, or dw itself."""
+    lib, dev = load_library(), _device()
+    (ot, (G, n, k)), (dt, shape) = _weights("dw", dw), _matrix_like("dy", dy)
+    rows = shape[0]
+    source = _source(a, rows, a_rows, k)
+    (pd, ldy), (pa, lda) = _matrix("dy", dy, dev, dt, (rows, n)), _matrix("a", a, dev, dt, source)
+    pf, pr = _grouped(dev, G, rows, offsets, a_rows)
+    padd, pw = _dense(dev, _WGRAD, dw_add, torch.float32, dw.shape, dw, ot, dw.shape)
+    _check(lib.moe_grouped_mm_wgrad(_ROW_TYPES[dt], G, n, k, rows, pd, ldy, pa, lda, pr, source[0], pf, padd,
+                                    _ROW_TYPES[ot], pw, _row_stream(stream, dev)), "moe_grouped_mm_wgrad")
+
+
+_WEIGHTS4 = ("codes", "scales")
+
+
+def _weights4(dev, name, t, codes, scales):
+    """(type, rows, cols, addresses of t, codes, scales) of a 4-bit weights call."""
+    if not isinstance(t, torch.Tensor) or t.dim() < 1 or t.dtype not in _ROW_TYPES:
+        raise ValueError(f"{name}: expected a tensor of float32, bfloat16 or float16")
+    cols = t.shape[-1]
+    cs, ss = weights4_shapes(t.shape)
+    ptrs = _dense(dev, (name, *_WEIGHTS4), t, t.dtype, t.shape, codes, torch.uint8, cs, scales, torch.uint8, ss)
+    return _ROW_TYPES[t.dtype], t.numel() // cols if cols else 0, cols, ptrs
+
+
+def moe_weights4_pack(w, codes, scales, stream=None):
+    """4-bit weights of w [..., cols] (float32, bfloat16 or float16, cols a multiple of 32):
+    codes uint8 [..., cols / 2], scales uint8 [..., cols / 32]."""
+    lib, dev = load_library(), _device()
+    dt, rows, cols, (pw, pc, ps) = _weights4(dev, "w", w, codes, scales)
+    _check(lib.moe_weights4_pack(rows, cols, dt, pw, pc, ps, _row_stream(stream, dev)), "moe_weights4_pack")
+
+
+def moe_weights4_unpack(codes, scales, out, stream=None):
+    """The values 4-bit weights stand for, into out [..., cols]."""
+    lib, dev = load_library(), _device()
+    dt, rows, cols, (po, pc, ps) = _weights4(dev, "out", out, codes, scales)
+    _check(lib.moe_weights4_unpack(rows, cols, dt, pc, ps, po, _row_stream(stream, dev)), "moe_weights4_unpack")
+
+
+_GEMM4 = ("codes0", "scales0", "codes1", "scales1")
+
+
+def moe_grouped_gemm4(op, a, offsets, codes0, scales0, out, codes1=None, scales1=None, a_rows=None, stream=None):
+    """moe_grouped_mm with 4-bit weights [experts][n][k]: out[p] = W0 a[p] (MOE_GEMM_DOWN) or
+    silu(W0 a[p]) * (W1 a[p]) (MOE_GEMM_GATE_UP), for the few rows of a decode step."""
+    lib, dev = load_library(), _device()
+    dt, (_, k) = _matrix_like("a", a)
+    ot, (rows, n) = _matrix_like("out", out)
+    if not isinstance(codes0, torch.Tensor) or codes0.dim() != 3:
+        raise ValueError("codes0: expected uint8 [groups][n_out][k_dim / 2]")
+    G = codes0.shape[0]
+    source = _source(a, rows, a_rows, k)
+    (pa, lda), (po, ldo) = _matrix("a", a, dev, dt, source), _matrix("out", out, dev, ot, (rows, n))
+    pf, pr = _grouped(dev, G, rows, offsets, a_rows)
+    if op != MOE_GEMM_GATE_UP:
+        codes1 = scales1 = None
+    u8, (cs, ss) = torch.uint8, weights4_shapes((G, n, k))
+    ptrs = _dense(dev, _GEMM4, codes0, u8, cs, scales0, u8, ss, codes1, u8, cs, scales1, u8, ss)
+    _check(lib.moe_grouped_gemm4(op, _ROW_TYPES[dt], G, n, k, rows, pa, lda, pr, source[0], pf, *ptrs, _ROW_TYPES[ot],
+                                 po, ldo, _row_stream(stream, dev)), "moe_grouped_gemm4")
 
 
 def moe_aux_stats(dims, logits, topk_idx, f, P, counts, scalars, ws, stream=None):

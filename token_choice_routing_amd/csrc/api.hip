@@ -764,6 +764,195 @@ moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_
   return MOE_OK;
 }
 
+// Grouped products. Sizes keep a tile's byte offsets in 32 bits (256 rows of 2^20 + row
+// spacing), row numbers in 31.
+static moe_status check_mm(int32_t dtype, int32_t out_dtype, int32_t groups, int32_t n_out, int32_t k_dim,
+                           int64_t rows, const int32_t* offsets) {
+  if (!row_dtype(dtype) || !row_dtype(out_dtype) || groups < 1 || n_out < 8 || n_out % 8 || k_dim < 8 || k_dim % 8 ||
+      rows < 0 || (!offsets && groups != 1))
+    return MOE_ERR_ARG;
+  if (groups > MOE_MAX_EXPERTS || n_out > MOE_MM_MAX_DIM || k_dim > MOE_MM_MAX_DIM || rows >= (int64_t(1) << 31) - 512)
+    return MOE_ERR_UNSUPPORTED;
+  // tiles are counted in 31 bits, whatever the offsets hold (each group all rows)
+  if (groups * (rows / 64 + 1) * (std::max(n_out, k_dim) / 64 + 1) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  return maybe(offsets);
+}
+// A matrix of `cols` columns whose rows are ld elements apart.
+static moe_status check_mm_rows(const void* p, int64_t ld, int32_t cols) {
+  if (ld < cols || ld % 8) return MOE_ERR_ARG;
+  if (ld > 2 * (int64_t)MOE_MM_MAX_DIM) return MOE_ERR_UNSUPPORTED;
+  return need(p);
+}
+// The rows operand, read through a_rows if there is one: then with 32-bit byte offsets.
+static moe_status check_mm_a(const void* a, int64_t lda, int32_t k_dim, const int32_t* a_rows, int64_t a_nrows,
+                             int32_t dtype, int64_t rows) {
+  MOE_TRY(check_mm_rows(a, lda, k_dim));
+  if (!a_rows) return MOE_OK;
+  if (a_nrows < 0 || (a_nrows == 0 && rows > 0)) return MOE_ERR_ARG;
+  if (a_nrows > 0xFFFFFFFFll / lda || (a_nrows + 1) * lda * (dtype == MOE_F32 ? 4 : 2) > 0xFFFFFFFFll)
+    return MOE_ERR_UNSUPPORTED;
+  return maybe(a_rows);
+}
+
+moe_status moe_grouped_mm(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows, const void* a,
+                          int64_t lda, const int32_t* a_rows, int64_t a_nrows, const int32_t* offsets, const void* w,
+                          int32_t out_dtype, void* out, int64_t ldo, moe_stream stream) {
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  MOE_TRY(check_mm_a(a, lda, k_dim, a_rows, a_nrows, dtype, rows));
+  MOE_TRY(need(w));
+  MOE_TRY(check_mm_rows(out, ldo, n_out));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  GroupedMm g{};
+  g.form = kMm;
+  g.dtype = dtype;
+  g.out_dtype = out_dtype;
+  g.groups = n_groups;
+  g.n_out = n_out;
+  g.k_dim = k_dim;
+  g.rows = rows;
+  g.offsets = offsets;
+  g.a = a;
+  g.lda = lda;
+  g.a_rows = a_rows;
+  g.a_nrows = a_nrows;
+  g.w = w;
+  g.out = out;
+  g.ldo = ldo;
+  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_mm_dgrad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
+                                const void* dy, int64_t ldy, const int32_t* offsets, const void* w, int32_t out_dtype,
+                                void* da, int64_t lda, moe_stream stream) {
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  MOE_TRY(check_mm_rows(dy, ldy, n_out));
+  MOE_TRY(need(w));
+  MOE_TRY(check_mm_rows(da, lda, k_dim));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  GroupedMm g{};
+  g.form = kMmDgrad;
+  g.dtype = dtype;
+  g.out_dtype = out_dtype;
+  g.groups = n_groups;
+  g.n_out = n_out;
+  g.k_dim = k_dim;
+  g.rows = rows;
+  g.offsets = offsets;
+  g.dy = dy;
+  g.ldy = ldy;
+  g.w = w;
+  g.out = da;
+  g.ldo = lda;
+  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_mm_wgrad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
+                                const void* dy, int64_t ldy, const void* a, int64_t lda, const int32_t* a_rows,
+                                int64_t a_nrows, const int32_t* offsets, const float* dw_add, int32_t out_dtype,
+                                void* dw, moe_stream stream) {
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  MOE_TRY(check_mm_rows(dy, ldy, n_out));
+  MOE_TRY(check_mm_a(a, lda, k_dim, a_rows, a_nrows, dtype, rows));
+  MOE_TRY(maybe(dw_add));
+  MOE_TRY(need(dw));
+  if (dw_add && dw_add == dw && out_dtype != MOE_F32) return MOE_ERR_ARG;  // in place: the same type
+  MOE_TRY(no_pending_error());
+  GroupedMm g{};
+  g.form = kMmWgrad;
+  g.dtype = dtype;
+  g.out_dtype = out_dtype;
+  g.groups = n_groups;
+  g.n_out = n_out;
+  g.k_dim = k_dim;
+  g.rows = rows;
+  g.offsets = offsets;
+  g.a = a;
+  g.lda = lda;
+  g.a_rows = a_rows;
+  g.a_nrows = a_nrows;
+  g.dy = dy;
+  g.ldy = ldy;
+  g.add = dw_add;
+  g.out = dw;
+  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
+                             const void* a, int64_t lda, const int32_t* a_rows, int64_t a_nrows,
+                             const int32_t* offsets, const uint8_t* codes0, const uint8_t* scales0,
+                             const uint8_t* codes1, const uint8_t* scales1, int32_t out_dtype, void* out, int64_t ldo,
+                             moe_stream stream) {
+  if (op != MOE_GEMM_GATE_UP && op != MOE_GEMM_DOWN) return MOE_ERR_ARG;
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  if (k_dim % 32) return MOE_ERR_ARG;
+  MOE_TRY(check_mm_a(a, lda, k_dim, a_rows, a_nrows, dtype, rows));
+  MOE_TRY(need(codes0));
+  MOE_TRY(need(scales0));
+  if (op == MOE_GEMM_GATE_UP) {
+    MOE_TRY(need(codes1));
+    MOE_TRY(need(scales1));
+  }
+  MOE_TRY(check_mm_rows(out, ldo, n_out));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  GroupedMm g{};
+  g.form = op == MOE_GEMM_GATE_UP ? kMm4Swiglu : kMm4;
+  g.dtype = dtype;
+  g.out_dtype = out_dtype;
+  g.groups = n_groups;
+  g.n_out = n_out;
+  g.k_dim = k_dim;
+  g.rows = rows;
+  g.offsets = offsets;
+  g.a = a;
+  g.lda = lda;
+  g.a_rows = a_rows;
+  g.a_nrows = a_nrows;
+  g.codes0 = codes0;
+  g.scales0 = scales0;
+  g.codes1 = codes1;
+  g.scales1 = scales1;
+  g.out = out;
+  g.ldo = ldo;
+  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+static moe_status check_weights4(int64_t rows, int32_t cols, int32_t dtype) {
+  if (rows < 0 || cols < 32 || cols % 32 || !row_dtype(dtype)) return MOE_ERR_ARG;
+  if (rows >= (int64_t(1) << 40) || rows * cols >= (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe_status moe_weights4_pack(int64_t rows, int32_t cols, int32_t dtype, const void* w, uint8_t* codes, uint8_t* scales,
+                             moe_stream stream) {
+  MOE_TRY(check_weights4(rows, cols, dtype));
+  MOE_TRY(need(w));
+  MOE_TRY(need(codes));
+  MOE_TRY(need(scales));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  HIP_TRY(launch_weights4_pack(dtype, w, rows * (cols / 32), codes, scales, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
+moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const uint8_t* codes, const uint8_t* scales,
+                               void* out, moe_stream stream) {
+  MOE_TRY(check_weights4(rows, cols, dtype));
+  MOE_TRY(need(codes));
+  MOE_TRY(need(scales));
+  MOE_TRY(need(out));
+  if (rows == 0) return MOE_OK;
+  MOE_TRY(no_pending_error());
+  HIP_TRY(launch_weights4_unpack(dtype, codes, scales, rows * (cols / 32), out, static_cast<hipStream_t>(stream)));
+  return MOE_OK;
+}
+
 moe_status moe_aux_stats(const moe_dims* d, const float* logits, const int32_t* topk_idx, float* f,
                          float* P, int32_t* counts, float* scalars, void* ws, size_t ws_bytes,
                          moe_stream stream) {

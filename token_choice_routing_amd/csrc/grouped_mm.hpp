@@ -1,0 +1,76 @@
+// Segments of a grouped product: which rows each group owns and which tile a workgroup
+// takes, from the offsets on the device.
+#pragma once
+#include "common.hpp"
+#include "kernels.hpp"
+
+namespace moe {
+
+constexpr int kMmGroups = MOE_MAX_EXPERTS;
+
+// Row ranges of the groups and the running count of their output tiles.
+struct Segments {
+  int start[kMmGroups + 1];
+  int len[kMmGroups + 1];
+  int prefix[kMmGroups + 1];  // tiles before group e
+};
+
+// Group e's rows are [a, b) with a = clamp(offsets[e], 0, rows), b = clamp(offsets[e + 1], a,
+// rows): inside the buffers whatever the offsets hold. A group has ceil(extent / bm) * nt
+// tiles, extent being its rows, or `fixed` where that is positive (a weight gradient: every
+// group's output has n_out rows). Called by the whole workgroup (at least one wavefront);
+// returns the number of tiles.
+__device__ __forceinline__ int build_segments(Segments& sg, const int32_t* offsets, int groups, int64_t rows, int bm,
+                                              int nt, int fixed) {
+  if (threadIdx.x < kWave) {
+    const int lane = threadIdx.x;
+    constexpr int kPer = (kMmGroups + kWave) / kWave;
+    int cnt[kPer], local = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int e = lane * kPer + q;
+      int64_t a = 0, b = 0;
+      if (e < groups) {
+        b = rows;
+        if (offsets) {
+          a = min<int64_t>(max<int64_t>(offsets[e], 0), rows);
+          b = min<int64_t>(max<int64_t>(offsets[e + 1], a), rows);
+        }
+      }
+      const int len = (int)(b - a);
+      if (e <= kMmGroups) {
+        sg.start[e] = (int)a;
+        sg.len[e] = len;
+      }
+      cnt[q] = e < groups ? ((fixed > 0 ? fixed : len) + bm - 1) / bm * nt : 0;
+      local += cnt[q];
+    }
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += v;
+    }
+    int run = incl - local;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      const int e = lane * kPer + q;
+      if (e <= kMmGroups) sg.prefix[e] = run;
+      run += cnt[q];
+    }
+  }
+  __syncthreads();
+  return sg.prefix[groups];
+}
+
+// The group of tile t (prefix[e] <= t < prefix[e + 1]).
+__device__ __forceinline__ int segment_of(const Segments& sg, int groups, int t) {
+  int lo = 0, hi = groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (sg.prefix[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+}  // namespace moe

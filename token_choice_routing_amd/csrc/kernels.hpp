@@ -311,6 +311,33 @@ struct SwigluBwd8Args {
 };
 hipError_t launch_swiglu_bwd8(const SwigluBwd8Args& a, hipStream_t s);
 
+// Products of rows in expert order with their expert's weights (grouped_mm.hip).
+enum { kMm = 0, kMmDgrad = 1, kMmWgrad = 2, kMm4 = 3, kMm4Swiglu = 4 };
+struct GroupedMm {
+  int form;
+  int dtype, out_dtype;     // moe_dtype of the operands and of out
+  int groups, n_out, k_dim;
+  int64_t rows;
+  const int32_t* offsets;   // [groups + 1] device, or NULL: one segment of rows rows
+  const void* a;            // product, weight gradient: [rows or a_nrows][lda]
+  int64_t lda;
+  const int32_t* a_rows;    // [rows] or NULL: row p reads a[a_rows[p]]
+  int64_t a_nrows;
+  const void* dy;           // gradients: [rows][ldy]
+  int64_t ldy;
+  const void* w;            // product, data gradient: [groups][n_out][k_dim]
+  const uint8_t *codes0, *scales0, *codes1, *scales1;  // 4-bit weights (1: the up weights)
+  const float* add;         // weight gradient: [groups][n_out][k_dim] or NULL
+  void* out;
+  int64_t ldo;              // (weight gradient: dense)
+};
+hipError_t launch_grouped_mm(const GroupedMm& g, hipStream_t s);
+
+// 4-bit weights (weights4.hip): blocks of 32 elements.
+hipError_t launch_weights4_pack(int dtype, const void* w, int64_t blocks, void* codes, void* scales, hipStream_t s);
+hipError_t launch_weights4_unpack(int dtype, const void* codes, const void* scales, int64_t blocks, void* out,
+                                  hipStream_t s);
+
 struct AuxArgs {
   int64_t T;
   int N, M, K;
