@@ -819,7 +819,7 @@ moe_status moe_grouped_mm(int32_t dtype, int32_t n_groups, int32_t n_out, int32_
   g.w = w;
   g.out = out;
   g.ldo = ldo;
-  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  HIP_TRY(launch_grouped_mm(g, cu_count(), static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 
@@ -846,7 +846,7 @@ moe_status moe_grouped_mm_dgrad(int32_t dtype, int32_t n_groups, int32_t n_out, 
   g.w = w;
   g.out = da;
   g.ldo = lda;
-  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  HIP_TRY(launch_grouped_mm(g, cu_count(), static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 
@@ -878,7 +878,7 @@ moe_status moe_grouped_mm_wgrad(int32_t dtype, int32_t n_groups, int32_t n_out, 
   g.ldy = ldy;
   g.add = dw_add;
   g.out = dw;
-  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  HIP_TRY(launch_grouped_mm(g, cu_count(), static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 
@@ -919,7 +919,7 @@ moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_
   g.scales1 = scales1;
   g.out = out;
   g.ldo = ldo;
-  HIP_TRY(launch_grouped_mm(g, static_cast<hipStream_t>(stream)));
+  HIP_TRY(launch_grouped_mm(g, cu_count(), static_cast<hipStream_t>(stream)));
   return MOE_OK;
 }
 

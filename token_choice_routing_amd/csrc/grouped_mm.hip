@@ -115,7 +115,8 @@ __global__ void __launch_bounds__(256) grouped_mm_kernel(GroupedMm g) {
 
 }  // namespace
 
-hipError_t launch_grouped_mm(const GroupedMm& g, hipStream_t s) {
+hipError_t launch_grouped_mm(const GroupedMm& g, int num_cus, hipStream_t s) {
+  if (g.dtype != MOE_F32 && g.form <= kMmWgrad) return launch_grouped_mm16(g, num_cus, s);
   const int I = g.form == kMmWgrad ? g.n_out : 0;
   const int J = g.form == kMmDgrad || g.form == kMmWgrad ? g.k_dim : g.n_out;
   const int64_t nt = (J + kT - 1) / kT;

@@ -331,7 +331,8 @@ struct GroupedMm {
   void* out;
   int64_t ldo;              // (weight gradient: dense)
 };
-hipError_t launch_grouped_mm(const GroupedMm& g, hipStream_t s);
+hipError_t launch_grouped_mm(const GroupedMm& g, int num_cus, hipStream_t s);
+hipError_t launch_grouped_mm16(const GroupedMm& g, int num_cus, hipStream_t s);  // 16-bit dtype, 16-bit weights
 
 // 4-bit weights (weights4.hip): blocks of 32 elements.
 hipError_t launch_weights4_pack(int dtype, const void* w, int64_t blocks, void* codes, void* scales, hipStream_t s);
