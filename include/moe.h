@@ -407,7 +407,7 @@ moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_
  * n_out and k_dim multiples of 8 up to MOE_MM_MAX_DIM, ld arguments (elements from one row
  * to the next) multiples of 8 up to twice that, n_groups up to MOE_MAX_EXPERTS, rows below
  * 2^31 - 512 and n_groups (rows / 64 + 1) (max(n_out, k_dim) / 64 + 1) below 2^31; with
- * a_rows, (a_nrows + 1) rows of lda elements must fit in 4 GB; else MOE_ERR_UNSUPPORTED.
+ * a_rows, (a_nrows + 1) rows of lda elements must fit in 4 GB - 256 B; else MOE_ERR_UNSUPPORTED.
  * No workspace. Outputs must not overlap inputs (except dw and dw_add) or each other.
  */
 #define MOE_MM_MAX_DIM (1 << 20)

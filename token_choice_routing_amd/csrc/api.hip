@@ -789,7 +789,7 @@ static moe_status check_mm_a(const void* a, int64_t lda, int32_t k_dim, const in
   MOE_TRY(check_mm_rows(a, lda, k_dim));
   if (!a_rows) return MOE_OK;
   if (a_nrows < 0 || (a_nrows == 0 && rows > 0)) return MOE_ERR_ARG;
-  if (a_nrows > 0xFFFFFFFFll / lda || (a_nrows + 1) * lda * (dtype == MOE_F32 ? 4 : 2) > 0xFFFFFFFFll)
+  if (a_nrows > 0xFFFFFF00ll / lda || (a_nrows + 1) * lda * (dtype == MOE_F32 ? 4 : 2) > 0xFFFFFF00ll)
     return MOE_ERR_UNSUPPORTED;
   return maybe(a_rows);
 }

@@ -9,9 +9,12 @@ namespace moe {
 
 namespace {
 
-constexpr int kBK = 32, kStages = 4;
+constexpr int kBK = 32;
 constexpr uint32_t kPast = 0xfffffff0u;     // byte offset past every resource: reads zero, touches nothing
 constexpr uint32_t kRecords = 0xffffff00u;  // (lanes that read anything are bounded by their own tests)
+
+constexpr int kBand = 8;  // row tiles
+constexpr int kStream = 2;  // cache policy of the output stores: not kept (nt)
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -22,17 +25,6 @@ __device__ __forceinline__ f32x16_t mfma16(bf16x8_t j, bf16x8_t i, f32x16_t c) {
   else
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, j), __builtin_bit_cast(f16x8_t, i), c, 0,
                                                   0, 0);
-}
-
-// v_permlane32_swap_b32: lane half 0 gets (a, a of the lane 32 on), half 1 (b of the lane 32
-// back, b).
-__device__ __forceinline__ u32x2_t swap_lane_halves(uint32_t a, uint32_t b) {
-#if defined(__HIP_DEVICE_COMPILE__)
-  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-  return u32x2_t{r[0], r[1]};
-#else
-  return u32x2_t{a, b};
-#endif
 }
 
 // A 4-element column of a K-major stage by the transposing LDS read: within each 16-lane
@@ -49,7 +41,15 @@ __device__ __forceinline__ s16x4_t read_tr(const char* __restrict__ p) {
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
-template <typename T, int FORM, int BM, int BN, int WM, int WN>
+// Calls f with n as a constant (0 <= n <= N, the same in every lane).
+template <int N, typename F>
+__device__ __forceinline__ void deal(int n, F&& f) {
+  if constexpr (N == 0) f(std::integral_constant<int, 0>{});
+  else if (n >= N) f(std::integral_constant<int, N>{});
+  else deal<N - 1>(n, f);
+}
+
+template <typename T, int FORM, int BM, int BN, int WM, int WN, int S>
 __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 grouped_mm16_kernel(GroupedMm g) {
   constexpr int NW = WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
@@ -58,7 +58,7 @@ grouped_mm16_kernel(GroupedMm g) {
   constexpr int PL = PI + PJ;
   constexpr int STAGE = (BM + BN) * kBK * 2;               // bytes
   __shared__ Segments sg;
-  extern __shared__ __attribute__((aligned(16))) char smem[];  // [kStages][I region, J region]
+  extern __shared__ __attribute__((aligned(16))) char smem[];  // [S][I region, J region]
   const int I = KI ? g.n_out : 0, J = FORM == kMm ? g.n_out : g.k_dim;
   const int nt = (J + BN - 1) / BN;
   const int total = build_segments(sg, g.offsets, g.groups, g.rows, BM, nt, I);
@@ -66,7 +66,8 @@ grouped_mm16_kernel(GroupedMm g) {
   const int wm = wave / WN, wn = wave % WN;  // (the wavefronts of a SIMD have different rows)
   const int half = lane >> 5, l32 = lane & 31;
 
-  // Tiles (expert, column tile, row tile), an eighth of the list for each XCD.
+  // Tiles (expert, band of row tiles, column tile, row tile), an eighth of the list for each
+  // XCD: the tiles it runs at once share weight panels and row panels in its L2.
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, per = gridDim.x >> 3;
   const int first = (int)((int64_t)xcd * total / 8), count = (int)((int64_t)(xcd + 1) * total / 8) - first;
 
@@ -82,9 +83,12 @@ grouped_mm16_kernel(GroupedMm g) {
     w.start = uniform(sg.start[w.e]);
     const int extent = KI ? I : len;
     const int mt = (extent + BM - 1) / BM;
-    w.j0 = local / mt * BN;
-    w.i0 = local % mt * BM;
-    w.iv = min(BM, extent - w.i0);
+    const int band = local / (kBand * nt), in = local - band * kBand * nt;
+    const int high = min(kBand, mt - band * kBand);
+    w.j0 = in / high * BN;
+    const int at = band * kBand + in % high, blocks = (extent + 31) / 32;
+    w.i0 = (int)((int64_t)at * blocks / mt) * 32;
+    w.iv = min((int)((int64_t)(at + 1) * blocks / mt) * 32, extent) - w.i0;
     w.jv = min(BN, J - w.j0);
     w.klen = KI ? len : FORM == kMmDgrad ? g.n_out : g.k_dim;
     return w;
@@ -100,13 +104,41 @@ grouped_mm16_kernel(GroupedMm g) {
     return ((p & 3) | (((p >> 2) ^ (kr & 3)) << 2)) * 8;
   };
 
-  // ---- the stream of K tiles, kStages ahead of the products, item after item
+  // ---- the stream of K tiles, S ahead of the products, item after item
   const T* isrc = nullptr;
   const T* jsrc = nullptr;
   uint32_t ioff[PI], joff[PJ];
   int lit = slot, lkt = 0, lnk = 0, lklen = 0, lstart = 0;
   int64_t istep = 0, jstep = 0;
   const uint32_t lda2 = (uint32_t)g.lda * 2;
+  // Gathered rows of the reduction: byte offsets of the rows that the wavefront's pieces of
+  // the next K tile hold (the same in every lane, read as scalars a tile ahead: vector loads
+  // return in order, so one would wait for every tile in flight).
+  constexpr int KPP = KJ ? 512 / BN : 1;
+  uint32_t idx[PJ][KPP];
+  typedef const __attribute__((address_space(4))) int32_t* scalar_rows;
+  const scalar_rows a_rows = (scalar_rows)(uintptr_t)g.a_rows;
+  auto fetch_rows = [&]() {
+#pragma unroll
+    for (int p = 0; p < PJ; ++p)
+#pragma unroll
+      for (int q = 0; q < KPP; ++q) {
+        const int k = min(lkt * kBK + (wave + NW * p) * KPP + q, lklen - 1);
+        const int64_t row = a_rows[uniform(lstart + k)];
+        idx[p][q] = (uint32_t)min<int64_t>(max<int64_t>(row, 0), g.a_nrows - 1) * lda2;
+      }
+  };
+  // Rows of the next item's I pieces in a gathered product, read an item ahead.
+  const bool gather = FORM == kMm && g.a_rows;
+  int32_t nrow[PI];
+  auto fetch_next = [&]() {
+    if (!gather || lit >= count) return;
+    const Item w = locate(lit);
+#pragma unroll
+    for (int p = 0; p < PI; ++p)
+      nrow[p] = g.a_rows[w.start + w.i0 + min(16 * (wave + NW * p) + (lane >> 2), w.iv - 1)];
+  };
+  fetch_next();
   auto open_item = [&]() {
     // the next item with anything to reduce over
     lkt = 0;
@@ -121,7 +153,6 @@ grouped_mm16_kernel(GroupedMm g) {
       lstart = w.start;
       const int64_t ild = FORM == kMm ? g.lda : g.ldy;
       const T* ibase = static_cast<const T*>(FORM == kMm ? g.a : g.dy);
-      const bool gather = FORM == kMm && g.a_rows;
       if (!gather) ibase += (int64_t)(w.start + (KI ? 0 : w.i0)) * ild + (KI ? w.i0 : 0);
       isrc = uniform_ptr(ibase);
       istep = KI ? kBK * ild : kBK;
@@ -133,7 +164,7 @@ grouped_mm16_kernel(GroupedMm g) {
         } else {
           const int r = 16 * (wave + NW * p) + (lane >> 2);
           int64_t row = r;
-          if (gather) row = min<int64_t>(max<int64_t>(g.a_rows[w.start + w.i0 + min(r, w.iv - 1)], 0), g.a_nrows - 1);
+          if (gather) row = min<int64_t>(max<int64_t>(nrow[p], 0), g.a_nrows - 1);
           ioff[p] = r < w.iv ? (uint32_t)(row * ild + lc * 8) * 2u : kPast;
         }
       }
@@ -155,6 +186,8 @@ grouped_mm16_kernel(GroupedMm g) {
           joff[p] = r < w.jv ? (uint32_t)(r * jld + lc * 8) * 2u : kPast;
         }
       }
+      if (FORM == kMmWgrad && g.a_rows) fetch_rows();
+      fetch_next();
       return;
     }
   };
@@ -175,10 +208,11 @@ grouped_mm16_kernel(GroupedMm g) {
       const int piece = wave + NW * p;
       const int k = k0 + (KJ ? krow(piece, BN) : lc * 8);
       uint32_t off = joff[p];
-      if (FORM == kMmWgrad && g.a_rows && lnk) {
-        const int64_t row = g.a_rows[lstart + min(k, lklen - 1)];
-        off += (uint32_t)min<int64_t>(max<int64_t>(row, 0), g.a_nrows - 1) * lda2;
-        if (joff[p] == kPast) off = kPast;
+      if (FORM == kMmWgrad && g.a_rows) {
+        uint32_t at = idx[p][0];
+#pragma unroll
+        for (int q = 1; q < KPP; ++q) at = lane / (BN / 8) >= q ? idx[p][q] : at;
+        off = off == kPast ? kPast : off + at;
       }
       buffer_load_lds16(rj, whole || k < lklen ? off : kPast,
                         reinterpret_cast<bf16_t*>(stage + BM * kBK * 2 + piece * 1024));
@@ -186,6 +220,7 @@ grouped_mm16_kernel(GroupedMm g) {
     isrc = uniform_ptr(isrc + istep);
     jsrc = uniform_ptr(jsrc + jstep);
     if (lkt < lnk) ++lkt;
+    if (FORM == kMmWgrad && g.a_rows && lkt < lnk) fetch_rows();
   };
 
   // ---- fragments: per 16-wide K step FN J blocks and FM I blocks of 32
@@ -195,11 +230,11 @@ grouped_mm16_kernel(GroupedMm g) {
     const int kl = 8 * half + (s16 >> 2), nl = 16 * ((lane >> 4) & 1) + 4 * (s16 & 3);
     if constexpr (KI) {
 #pragma unroll
-      for (int b = 0; b < FM; ++b) iaddr[b] = (uint32_t)(kl * BM + (((wm * FM + b) ^ (kl & 3)) * 32) + nl) * 2;
+      for (int b = 0; b < FM; ++b) iaddr[b] = (uint32_t)(kl * BM + (((b * WM + wm) ^ (kl & 3)) * 32) + nl) * 2;
     } else {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        iaddr[ks] = (uint32_t)((wm * FM * 32 + l32) * kBK + (((2 * ks + half) ^ ((l32 >> 2) & 3)) << 3)) * 2;
+        iaddr[ks] = (uint32_t)((wm * 32 + l32) * kBK + (((2 * ks + half) ^ ((l32 >> 2) & 3)) << 3)) * 2;
     }
     if constexpr (KJ) {
 #pragma unroll
@@ -218,7 +253,8 @@ grouped_mm16_kernel(GroupedMm g) {
     const s16x4_t lo = read_tr(p + ks * 16 * B * 2), hi = read_tr(p + (ks * 16 + 4) * B * 2);
     return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  auto read = [&](int st, int ks, Frags& f) {
+  auto read = [&](auto blocks, int st, int ks, Frags& f) {
+    constexpr int NB = decltype(blocks)::value;
     const char* stage = smem + st * STAGE;
 #pragma unroll
     for (int b = 0; b < FN; ++b) {
@@ -226,105 +262,174 @@ grouped_mm16_kernel(GroupedMm g) {
       else f.j[b] = *reinterpret_cast<const bf16x8_t*>(stage + jaddr[ks] + b * 32 * kBK * 2);
     }
 #pragma unroll
-    for (int b = 0; b < FM; ++b) {
+    for (int b = 0; b < NB; ++b) {
       if constexpr (KI) f.i[b] = column(stage + iaddr[b], ks, BM);
-      else f.i[b] = *reinterpret_cast<const bf16x8_t*>(stage + iaddr[ks] + b * 32 * kBK * 2);
+      else f.i[b] = *reinterpret_cast<const bf16x8_t*>(stage + iaddr[ks] + b * WM * 32 * kBK * 2);
+    }
+  };
+
+  // ---- outputs. In the products' layout a lane holds 16 columns of one row; a store of 16
+  // bytes a lane would touch 32 rows, and a CU then writes 37 GB/s. Turned round in LDS (8 rows
+  // of 128 bytes a 1 KB piece, 16-byte chunks XOR-ed with the row), eight lanes store 128
+  // bytes of a row: 115 GB/s. Rows and columns past the tile's get an offset past the resource.
+  auto out_at = [&](const Item& w) {  // the tile's first element
+    return KI ? ((int64_t)w.e * g.n_out + w.i0) * g.k_dim + w.j0 : (int64_t)(w.start + w.i0) * g.ldo + w.j0;
+  };
+  auto piece_at = [&](char* stage, int i) {
+    return stage + (i < PI ? wave + NW * i : BM / 16 + wave + NW * (i - PI)) * 1024;
+  };
+  // OT: the output type (float: 32-column blocks; uint32_t: 16-bit ones, 64 columns at a time
+  // but in 32s with ADD, whose addends are float32).
+  auto store = [&](auto type, auto added, const Item& w, const f32x16_t (&acc)[FN][FM], char* stage) {
+    typedef decltype(type) OT;
+    constexpr bool ADD = decltype(added)::value, WIDE = std::is_same<OT, float>::value || ADD;
+    constexpr int C = WIDE ? 1 : 2;  // 32-column blocks at a time
+    const int lane = opaque_v((int)threadIdx.x) & (kWave - 1), half = lane >> 5, l32 = lane & 31;
+    const int r8 = lane >> 3, c8 = lane & 7;
+    char* const mine[4] = {piece_at(stage, 0), piece_at(stage, 1), piece_at(stage, 2), piece_at(stage, 3)};
+    // this lane's row of a 32-row block, and the piece rows it reads back
+    char* const put = (l32 < 8 ? mine[0] : l32 < 16 ? mine[1] : l32 < 24 ? mine[2] : mine[3]) + (l32 & 7) * 128;
+    const int get = r8 * 128 + ((c8 ^ r8) << 4);
+    const int64_t at = out_at(w);
+    const auto ro = buffer_rsrc(uniform_ptr(static_cast<const OT*>(g.out) + at), kRecords);
+    const auto ra = buffer_rsrc(uniform_ptr(g.add + (ADD ? at : 0)), kRecords);
+    const uint32_t ld = (uint32_t)(KI ? g.k_dim : g.ldo);
+    auto pack = [](float x, float y) {
+      return std::is_same<OT, half_t>::value ? pack_f16x2(x, y) : cvt_bf16x2(x, y);
+    };
+#pragma unroll
+    for (int b = 0; b < FM; ++b) {
+#pragma unroll
+      for (int f = 0; f < FN; f += C) {
+#pragma unroll
+        for (int h = 0; h < C; ++h)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16_t& v = acc[f + h][b];
+            const f32x4_t x = {v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+            if constexpr (WIDE)
+              *reinterpret_cast<f32x4_t*>(put + (((2 * q + half) ^ (l32 & 7)) << 4)) = x;
+            else
+              *reinterpret_cast<u32x2_t*>(put + (((4 * h + q) ^ (l32 & 7)) << 4) + 8 * half) =
+                  u32x2_t{pack(x[0], x[1]), pack(x[2], x[3])};
+          }
+        const int c = wn * FN * 32 + f * 32 + 4 * C * c8;
+        u32x4_t x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const u32x4_t*>(mine[i] + get);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = (b * WM + wm) * 32 + 8 * i + r8;
+          const bool in = r < w.iv && c < w.jv;
+          const uint32_t el = (uint32_t)r * ld + (uint32_t)c;
+          if constexpr (ADD) {
+            const f32x4_t y =
+                __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ra, in ? el * 4u : kPast, 0, 0));
+            const f32x4_t z = __builtin_bit_cast(f32x4_t, x[i]) + y;
+            if constexpr (std::is_same<OT, float>::value)
+              x[i] = __builtin_bit_cast(u32x4_t, z);
+            else
+              x[i] = u32x4_t{pack(z[0], z[1]), pack(z[2], z[3]), 0, 0};
+          }
+          const uint32_t off = in ? el * (uint32_t)sizeof(OT) : kPast;
+          if constexpr (ADD && sizeof(OT) == 2)
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{x[i][0], x[i][1]}, ro, off, 0, kStream);
+          else
+            __builtin_amdgcn_raw_buffer_store_b128(x[i], ro, off, 0, kStream);
+        }
+      }
+    }
+  };
+  auto store_as = [&](const Item& w, const f32x16_t (&acc)[FN][FM], char* stage) {
+    auto typed = [&](auto type) {
+      if constexpr (KI) {
+        if (g.add) {
+          store(type, std::true_type{}, w, acc, stage);
+          return;
+        }
+      }
+      store(type, std::false_type{}, w, acc, stage);
+    };
+    if (g.out_dtype == MOE_F32) typed(float{});
+    else if (g.out_dtype == MOE_BF16) typed(bf16_t{});
+    else typed(half_t{});
+  };
+  // The output of an expert without rows: what is added, or zeros.
+  auto store_zero = [&](const Item& w) {
+    for (int i = lane; i < FM * 32 * FN * 4; i += kWave) {
+      const int r = (i / (FN * 4 * 32) * WM + wm) * 32 + i / (FN * 4) % 32, col = w.j0 + wn * FN * 32 + i % (FN * 4) * 8;
+      if (r >= w.iv || col >= J) continue;
+      const int64_t at = ((int64_t)w.e * g.n_out + w.i0 + r) * g.k_dim + col;
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      if (KI && g.add) load_row<8>(g.add + at, v);
+      if (g.out_dtype == MOE_F32) store_row<8>(static_cast<float*>(g.out) + at, v);
+      else if (g.out_dtype == MOE_BF16) store_row<8>(static_cast<bf16_t*>(g.out) + at, v);
+      else store_row<8>(static_cast<half_t*>(g.out) + at, v);
     }
   };
 
   if (slot >= count) return;
 #pragma unroll
-  for (int s = 0; s < kStages; ++s) issue(s);
-  wait_vmcnt<(kStages - 1) * PL>();
+  for (int s = 0; s < S; ++s) issue(s);
+  wait_vmcnt<(S - 1) * PL>();
   stage_barrier();
   int st = 0;
   for (int it = slot; it < count; it += per) {
     const Item w = locate(it);
-    const bool on = wm * FM * 32 < w.iv && wn * FN * 32 < w.jv;
+    // 32-row blocks of the tile, dealt out to the WM wavefronts of a column: a short tile
+    // leaves every SIMD the same share
+    const int mine = wn * FN * 32 < w.jv ? max(0, ((w.iv + 31) / 32 - wm + WM - 1) / WM) : 0;
     f32x16_t acc[FN][FM];
 #pragma unroll
     for (int f = 0; f < FN; ++f)
 #pragma unroll
       for (int b = 0; b < FM; ++b) acc[f][b] = f32x16_t{};
-    auto multiply = [&](const Frags& f) {
-#pragma unroll
-      for (int j = 0; j < FN; ++j)
-#pragma unroll
-        for (int b = 0; b < FM; ++b) acc[j][b] = mfma16<T>(f.j[j], f.i[b], acc[j][b]);
-    };
     const int nk = (w.klen + kBK - 1) / kBK;
-    Frags f0, f1;
-    if (on && nk) read(st, 0, f0);
-    for (int kt = 0; kt < nk; ++kt) {
-      const int next = (st + 1) & (kStages - 1);
-      if (on) {
-        read(st, 1, f1);
-        multiply(f0);
+    auto reduce = [&](auto blocks) {
+      constexpr int NB = decltype(blocks)::value;
+      auto multiply = [&](const Frags& f) {
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[j][b] = mfma16<T>(f.j[j], f.i[b], acc[j][b]);
+      };
+      Frags f0, f1;
+      if (NB && nk) read(blocks, st, 0, f0);
+      for (int kt = 0; kt < nk; ++kt) {
+        const int next = st + 1 == S ? 0 : st + 1;
+        if (NB) {
+          read(blocks, st, 1, f1);
+          multiply(f0);
+        }
+        // the next tile of the stream has landed, and every wavefront is done with this one
+        wait_vmcnt<(S - 2) * PL>();
+        stage_barrier();
+        if (kt + 1 < nk) {
+          issue(st);
+          if (NB) read(blocks, next, 0, f0);
+        }
+        if (NB) multiply(f1);
+        if (kt + 1 < nk) st = next;
       }
-      // the next tile of the stream has landed, and every wavefront is done with this one
-      wait_vmcnt<(kStages - 2) * PL>();
-      stage_barrier();
+    };
+    deal<FM>(mine, reduce);
+    // The stage of the last tile is free: each wavefront turns its outputs round in the pieces
+    // of it that it loads itself, then loads them.
+    if (mine && nk) store_as(w, acc, smem + st * STAGE);
+    if (mine && !nk) store_zero(w);  // (only a weight gradient has such items)
+    if (nk) {
       issue(st);
-      if (on) {
-        if (kt + 1 < nk) read(next, 0, f0);
-        multiply(f1);
-      }
-      st = next;
-    }
-    if (!on) continue;
-#pragma unroll
-    for (int b = 0; b < FM; ++b) {
-      const int r = wm * FM * 32 + b * 32 + l32;
-      if (r >= w.iv) continue;
-      const int64_t row = KI ? ((int64_t)w.e * g.n_out + w.i0 + r) * g.k_dim : (int64_t)(w.start + w.i0 + r) * g.ldo;
-#pragma unroll
-      for (int f = 0; f < FN; ++f) {
-        const int c0 = w.j0 + wn * FN * 32 + f * 32;
-        f32x16_t v = acc[f][b];
-        if (KI && g.add) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int col = c0 + 8 * q + 4 * half;
-            if (col >= J) continue;
-            const f32x4_t a = *reinterpret_cast<const f32x4_t*>(g.add + row + col);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[4 * q + j] += a[j];
-          }
-        }
-        if (g.out_dtype == MOE_F32) {
-          float* out = static_cast<float*>(g.out) + row;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int col = c0 + 8 * q + 4 * half;
-            if (col < J) *reinterpret_cast<f32x4_t*>(out + col) = f32x4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-          }
-          continue;
-        }
-        uint32_t p[8];
-        if (g.out_dtype == MOE_BF16) {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) p[q] = cvt_bf16x2(v[2 * q], v[2 * q + 1]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) p[q] = pack_f16x2(v[2 * q], v[2 * q + 1]);
-        }
-        // lane halves exchanged: 16 neighbouring columns a lane
-        uint16_t* out = static_cast<uint16_t*>(g.out) + row;
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          const u32x2_t x = swap_lane_halves(p[2 * q], p[2 * q + 4]), y = swap_lane_halves(p[2 * q + 1], p[2 * q + 5]);
-          const int col = c0 + 16 * half + 8 * q;
-          if (col < J) *reinterpret_cast<u32x4_t*>(out + col) = u32x4_t{x[0], y[0], x[1], y[1]};
-        }
-      }
+      st = st + 1 == S ? 0 : st + 1;
     }
   }
   wait_vmcnt<0>();  // the stream's last loads land before the workgroup's LDS is given away
 }
 
-template <typename T, int BM, int BN, int WM, int WN>
+template <typename T, int BM, int BN, int WM, int WN, int S>
 hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
-  constexpr size_t lds = (size_t)kStages * (BM + BN) * kBK * 2;
+  constexpr size_t lds = (size_t)S * (BM + BN) * kBK * 2;
   const int J = g.form == kMm ? g.n_out : g.k_dim;
   const int64_t nt = (J + BN - 1) / BN;
   const int64_t mt = g.form == kMmWgrad ? (int64_t)g.groups * ((g.n_out + BM - 1) / BM) : g.rows / BM + g.groups;
@@ -337,9 +442,9 @@ hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
     return hipGetLastError();
   };
   switch (g.form) {
-    case kMm: return go(grouped_mm16_kernel<T, kMm, BM, BN, WM, WN>);
-    case kMmDgrad: return go(grouped_mm16_kernel<T, kMmDgrad, BM, BN, WM, WN>);
-    case kMmWgrad: return go(grouped_mm16_kernel<T, kMmWgrad, BM, BN, WM, WN>);
+    case kMm: return go(grouped_mm16_kernel<T, kMm, BM, BN, WM, WN, S>);
+    case kMmDgrad: return go(grouped_mm16_kernel<T, kMmDgrad, BM, BN, WM, WN, S>);
+    case kMmWgrad: return go(grouped_mm16_kernel<T, kMmWgrad, BM, BN, WM, WN, S>);
   }
   return hipErrorInvalidValue;
 }
@@ -347,8 +452,8 @@ hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_grouped_mm16(const GroupedMm& g, int num_cus, hipStream_t s) {
-  return g.dtype == MOE_BF16 ? launch_tiles<bf16_t, 256, 256, 2, 4>(g, num_cus, s)
-                             : launch_tiles<half_t, 256, 256, 2, 4>(g, num_cus, s);
+  return g.dtype == MOE_BF16 ? launch_tiles<bf16_t, 256, 256, 2, 4, 4>(g, num_cus, s)
+                             : launch_tiles<half_t, 256, 256, 2, 4, 4>(g, num_cus, s);
 }
 
 }  // namespace moe
