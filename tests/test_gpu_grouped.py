@@ -107,6 +107,29 @@ def test_products(shape, dtype):
             check(dw, ref, mag, max(counts), out, "dw")
 
 
+# as many tiles as the 256 x 256 ones are taken for, with every number of 32-row blocks in them
+MANY = [0, 1, 31, 33, 64, 65, 129, 160, 200, 255, 256, 257, 300, 400, 513, 3] * 4
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("n,k,out", [(1032, 1040, "f32"), (1288, 1048, "bf16"), (1024, 2048, "f16")])
+def test_many_tiles(n, k, out, gather, dtype):
+    say(f"many tiles n {n} k {k} {dtype} -> {out} gather {gather}")
+    rows, off, a_rows, a, dy, w = make(31, MANY, n, k, dtype, T=900 if gather else None)
+    dw, add = kept(w.shape, out), None
+    if n == 1288:
+        add = torch.randn(w.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    y, da = kept((rows, n), out), kept((rows, k), out)
+    tcr.moe_grouped_mm(a, off, w, y, a_rows=a_rows)
+    tcr.moe_grouped_mm_dgrad(dy, off, w, da)
+    tcr.moe_grouped_mm_wgrad(dy, a, off, dw, a_rows=a_rows, dw_add=add)
+    ha, hf, hw, hr, hd, hadd = arrays(a, off, w, a_rows, dy, add)
+    check(y, *G.product(ha, hf, hw, rows, hr), k, out, "out")
+    check(da, *G.data_gradient(hd, hf, hw), n, out, "da")
+    check(dw, *G.weight_gradient(hd, ha, hf, len(MANY), hadd, hr), max(MANY) + 1, out, "dw")
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("counts,n,k", [([40, 0, 3], 72, 64), ([530, 300], 264, 520)])
 def test_spaced_rows(dtype, counts, n, k):

@@ -14,7 +14,6 @@ constexpr uint32_t kPast = 0xfffffff0u;     // byte offset past every resource: 
 constexpr uint32_t kRecords = 0xffffff00u;  // (lanes that read anything are bounded by their own tests)
 
 constexpr int kBand = 8;  // row tiles
-constexpr int kStream = 2;  // cache policy of the output stores: not kept (nt)
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
@@ -74,7 +73,7 @@ grouped_mm16_kernel(GroupedMm g) {
   struct Item {
     int e, start, i0, iv, j0, jv, klen;  // valid rows and columns of the tile; length of the reduction
   };
-  auto locate = [&](int it) {
+  auto locate = [&](int it) __attribute__((always_inline)) {
     Item w;
     const int t = first + it;
     w.e = uniform(segment_of(sg, g.groups, t));
@@ -98,8 +97,8 @@ grouped_mm16_kernel(GroupedMm g) {
   // row lane / 4 (chunks XOR-ed with (row / 4) % 4 against bank conflicts). K-major: 512 / B
   // K rows of B columns, 64-byte groups XOR-ed with the K row.
   const int lc = (lane & 3) ^ (lane >> 4);
-  auto krow = [&](int piece, int B) { return piece * (512 / B) + lane / (B / 8); };
-  auto kcol = [&](int kr, int B) {
+  auto krow = [&](int piece, int B) __attribute__((always_inline)) { return piece * (512 / B) + lane / (B / 8); };
+  auto kcol = [&](int kr, int B) __attribute__((always_inline)) {
     const int p = lane % (B / 8);
     return ((p & 3) | (((p >> 2) ^ (kr & 3)) << 2)) * 8;
   };
@@ -111,27 +110,27 @@ grouped_mm16_kernel(GroupedMm g) {
   int lit = slot, lkt = 0, lnk = 0, lklen = 0, lstart = 0;
   int64_t istep = 0, jstep = 0;
   const uint32_t lda2 = (uint32_t)g.lda * 2;
-  // Gathered rows of the reduction: byte offsets of the rows that the wavefront's pieces of
+  // Gathered rows of the reduction: the rows that the wavefront's pieces of
   // the next K tile hold (the same in every lane, read as scalars a tile ahead: vector loads
   // return in order, so one would wait for every tile in flight).
   constexpr int KPP = KJ ? 512 / BN : 1;
-  uint32_t idx[PJ][KPP];
+  int32_t idx[PJ][KPP];
+  const int last_row = (int)g.a_nrows - 1;  // ((a_nrows + 1) lda 2 bytes fit in 32 bits)
   typedef const __attribute__((address_space(4))) int32_t* scalar_rows;
   const scalar_rows a_rows = (scalar_rows)(uintptr_t)g.a_rows;
-  auto fetch_rows = [&]() {
+  auto fetch_rows = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int p = 0; p < PJ; ++p)
 #pragma unroll
       for (int q = 0; q < KPP; ++q) {
         const int k = min(lkt * kBK + (wave + NW * p) * KPP + q, lklen - 1);
-        const int64_t row = a_rows[uniform(lstart + k)];
-        idx[p][q] = (uint32_t)min<int64_t>(max<int64_t>(row, 0), g.a_nrows - 1) * lda2;
+        idx[p][q] = a_rows[(uint32_t)uniform(lstart + k)];
       }
   };
   // Rows of the next item's I pieces in a gathered product, read an item ahead.
   const bool gather = FORM == kMm && g.a_rows;
   int32_t nrow[PI];
-  auto fetch_next = [&]() {
+  auto fetch_next = [&]() __attribute__((always_inline)) {
     if (!gather || lit >= count) return;
     const Item w = locate(lit);
 #pragma unroll
@@ -139,7 +138,7 @@ grouped_mm16_kernel(GroupedMm g) {
       nrow[p] = g.a_rows[w.start + w.i0 + min(16 * (wave + NW * p) + (lane >> 2), w.iv - 1)];
   };
   fetch_next();
-  auto open_item = [&]() {
+  auto open_item = [&]() __attribute__((always_inline)) {
     // the next item with anything to reduce over
     lkt = 0;
     lnk = 0;
@@ -191,7 +190,7 @@ grouped_mm16_kernel(GroupedMm g) {
       return;
     }
   };
-  auto issue = [&](int st) {
+  auto issue = [&](int st) __attribute__((always_inline)) {
     if (lkt == lnk) open_item();
     char* stage = smem + st * STAGE;
     const auto ri = buffer_rsrc(isrc, kRecords), rj = buffer_rsrc(jsrc, kRecords);
@@ -209,10 +208,10 @@ grouped_mm16_kernel(GroupedMm g) {
       const int k = k0 + (KJ ? krow(piece, BN) : lc * 8);
       uint32_t off = joff[p];
       if (FORM == kMmWgrad && g.a_rows) {
-        uint32_t at = idx[p][0];
+        int row = idx[p][0];
 #pragma unroll
-        for (int q = 1; q < KPP; ++q) at = lane / (BN / 8) >= q ? idx[p][q] : at;
-        off = off == kPast ? kPast : off + at;
+        for (int q = 1; q < KPP; ++q) row = lane / (BN / 8) >= q ? idx[p][q] : row;
+        off = off == kPast ? kPast : off + (uint32_t)min(max(row, 0), last_row) * lda2;
       }
       buffer_load_lds16(rj, whole || k < lklen ? off : kPast,
                         reinterpret_cast<bf16_t*>(stage + BM * kBK * 2 + piece * 1024));
@@ -220,7 +219,15 @@ grouped_mm16_kernel(GroupedMm g) {
     isrc = uniform_ptr(isrc + istep);
     jsrc = uniform_ptr(jsrc + jstep);
     if (lkt < lnk) ++lkt;
-    if (FORM == kMmWgrad && g.a_rows && lkt < lnk) fetch_rows();
+  };
+  // Before each issue() but the first of an item. In the K loop the fragments read before are
+  // waited for first: scalar loads return in no order, so an LDS wait behind them would be one
+  // for everything.
+  auto before_issue = [&]() __attribute__((always_inline)) {
+    if (FORM == kMmWgrad && g.a_rows) {
+      __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4));  // lgkmcnt(0)
+      if (lkt < lnk) fetch_rows();
+    }
   };
 
   // ---- fragments: per 16-wide K step FN J blocks and FM I blocks of 32
@@ -249,11 +256,11 @@ grouped_mm16_kernel(GroupedMm g) {
   struct Frags {
     bf16x8_t j[FN], i[FM];
   };
-  auto column = [&](const char* p, int ks, int B) {
+  auto column = [&](const char* p, int ks, int B) __attribute__((always_inline)) {
     const s16x4_t lo = read_tr(p + ks * 16 * B * 2), hi = read_tr(p + (ks * 16 + 4) * B * 2);
     return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  auto read = [&](auto blocks, int st, int ks, Frags& f) {
+  auto read = [&](auto blocks, int st, int ks, Frags& f) __attribute__((always_inline)) {
     constexpr int NB = decltype(blocks)::value;
     const char* stage = smem + st * STAGE;
 #pragma unroll
@@ -272,18 +279,19 @@ grouped_mm16_kernel(GroupedMm g) {
   // bytes a lane would touch 32 rows, and a CU then writes 37 GB/s. Turned round in LDS (8 rows
   // of 128 bytes a 1 KB piece, 16-byte chunks XOR-ed with the row), eight lanes store 128
   // bytes of a row: 115 GB/s. Rows and columns past the tile's get an offset past the resource.
-  auto out_at = [&](const Item& w) {  // the tile's first element
+  auto out_at = [&](const Item& w) __attribute__((always_inline)) {  // the tile's first element
     return KI ? ((int64_t)w.e * g.n_out + w.i0) * g.k_dim + w.j0 : (int64_t)(w.start + w.i0) * g.ldo + w.j0;
   };
-  auto piece_at = [&](char* stage, int i) {
+  auto piece_at = [&](char* stage, int i) __attribute__((always_inline)) {
     return stage + (i < PI ? wave + NW * i : BM / 16 + wave + NW * (i - PI)) * 1024;
   };
   // OT: the output type (float: 32-column blocks; uint32_t: 16-bit ones, 64 columns at a time
   // but in 32s with ADD, whose addends are float32).
-  auto store = [&](auto type, auto added, const Item& w, const f32x16_t (&acc)[FN][FM], char* stage) {
+  auto store = [&](auto type, auto added, auto stream, const Item& w, const f32x16_t (&acc)[FN][FM], char* stage) __attribute__((always_inline)) {
     typedef decltype(type) OT;
     constexpr bool ADD = decltype(added)::value, WIDE = std::is_same<OT, float>::value || ADD;
     constexpr int C = WIDE ? 1 : 2;  // 32-column blocks at a time
+    constexpr int kPolicy = decltype(stream)::value ? 2 : 0;  // nt: not kept in the caches
     const int lane = opaque_v((int)threadIdx.x) & (kWave - 1), half = lane >> 5, l32 = lane & 31;
     const int r8 = lane >> 3, c8 = lane & 7;
     char* const mine[4] = {piece_at(stage, 0), piece_at(stage, 1), piece_at(stage, 2), piece_at(stage, 3)};
@@ -333,22 +341,26 @@ grouped_mm16_kernel(GroupedMm g) {
           }
           const uint32_t off = in ? el * (uint32_t)sizeof(OT) : kPast;
           if constexpr (ADD && sizeof(OT) == 2)
-            __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{x[i][0], x[i][1]}, ro, off, 0, kStream);
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{x[i][0], x[i][1]}, ro, off, 0, kPolicy);
           else
-            __builtin_amdgcn_raw_buffer_store_b128(x[i], ro, off, 0, kStream);
+            __builtin_amdgcn_raw_buffer_store_b128(x[i], ro, off, 0, kPolicy);
         }
       }
     }
   };
-  auto store_as = [&](const Item& w, const f32x16_t (&acc)[FN][FM], char* stage) {
-    auto typed = [&](auto type) {
+  auto store_as = [&](const Item& w, const f32x16_t (&acc)[FN][FM], char* stage) __attribute__((always_inline)) {
+    // A weight gradient is larger than the caches and written once: its lines are not kept, if
+    // they are whole ones (64 x 1536 x 2048 float32: 305 -> 280 us; with rows of 3104 bytes
+    // kept ones take 50 us and others 99).
+    auto typed = [&](auto type) __attribute__((always_inline)) {
       if constexpr (KI) {
-        if (g.add) {
-          store(type, std::true_type{}, w, acc, stage);
-          return;
-        }
+        const bool whole = (g.k_dim * sizeof(type)) % 128 == 0 && reinterpret_cast<uintptr_t>(g.out) % 128 == 0;
+        if (g.add) store(type, std::true_type{}, std::false_type{}, w, acc, stage);
+        else if (whole) store(type, std::false_type{}, std::true_type{}, w, acc, stage);
+        else store(type, std::false_type{}, std::false_type{}, w, acc, stage);
+      } else {
+        store(type, std::false_type{}, std::false_type{}, w, acc, stage);
       }
-      store(type, std::false_type{}, w, acc, stage);
     };
     if (g.out_dtype == MOE_F32) typed(float{});
     else if (g.out_dtype == MOE_BF16) typed(bf16_t{});
@@ -372,7 +384,10 @@ grouped_mm16_kernel(GroupedMm g) {
 
   if (slot >= count) return;
 #pragma unroll
-  for (int s = 0; s < S; ++s) issue(s);
+  for (int s = 0; s < S; ++s) {
+    before_issue();
+    issue(s);
+  }
   wait_vmcnt<(S - 1) * PL>();
   stage_barrier();
   int st = 0;
@@ -387,9 +402,9 @@ grouped_mm16_kernel(GroupedMm g) {
 #pragma unroll
       for (int b = 0; b < FM; ++b) acc[f][b] = f32x16_t{};
     const int nk = (w.klen + kBK - 1) / kBK;
-    auto reduce = [&](auto blocks) {
+    auto reduce = [&](auto blocks) __attribute__((always_inline)) {
       constexpr int NB = decltype(blocks)::value;
-      auto multiply = [&](const Frags& f) {
+      auto multiply = [&](const Frags& f) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -399,6 +414,7 @@ grouped_mm16_kernel(GroupedMm g) {
       if (NB && nk) read(blocks, st, 0, f0);
       for (int kt = 0; kt < nk; ++kt) {
         const int next = st + 1 == S ? 0 : st + 1;
+        before_issue();
         if (NB) {
           read(blocks, st, 1, f1);
           multiply(f0);
@@ -449,11 +465,26 @@ hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
   return hipErrorInvalidValue;
 }
 
+// Tiles of 128 x 128 (two workgroups a CU) where 256 x 256 would leave CUs idle, and for a
+// product of so few rows that it reads its weights once whatever the tile. us with 256 and 128:
+//   product 1024 rows of 8 experts, 1536 x 2048: 34 and 25; 1024 of 64: 105 and 88, 9600 of 64:
+//   126 and 137, 32768 of 8, 1024 x 1024: 72 and 98
+//   data gradient 1024 of 8: 29 and 21, 9600 of 64: 97 and 141 (and 73 and 78 at 1024 of 64)
+//   weight gradient 32768 of 8, 1024 x 1024 (128 tiles of 256 x 256): 100 and 80; 16384 of 1, 1536 x
+//   2048: 346 and 177; 16372 of 64, 768 x 1024 (768 tiles): 60 and 103
+template <typename T>
+hipError_t launch_for(const GroupedMm& g, int num_cus, hipStream_t s) {
+  const int64_t nt = ((g.form == kMm ? g.n_out : g.k_dim) + 255) / 256;
+  const int64_t mt = g.form == kMmWgrad ? (int64_t)g.groups * ((g.n_out + 255) / 256) : g.rows / 256 + g.groups;
+  const bool small = g.form == kMmWgrad ? mt * nt < 2 * num_cus
+                                        : mt * nt < num_cus || (g.form == kMm && g.rows <= 64 * (int64_t)g.groups);
+  return small ? launch_tiles<T, 128, 128, 2, 2, 4>(g, num_cus, s) : launch_tiles<T, 256, 256, 2, 4, 4>(g, num_cus, s);
+}
+
 }  // namespace
 
 hipError_t launch_grouped_mm16(const GroupedMm& g, int num_cus, hipStream_t s) {
-  return g.dtype == MOE_BF16 ? launch_tiles<bf16_t, 256, 256, 2, 4, 4>(g, num_cus, s)
-                             : launch_tiles<half_t, 256, 256, 2, 4, 4>(g, num_cus, s);
+  return g.dtype == MOE_BF16 ? launch_for<bf16_t>(g, num_cus, s) : launch_for<half_t>(g, num_cus, s);
 }
 
 }  // namespace moe
