@@ -449,7 +449,8 @@ moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const 
  *   op = MOE_GEMM_DOWN:    out[p] = W0[e] a[src(p)]          (codes1, scales1 unused)
  * W0 (and W1) are what codes [n_groups][n_out][k_dim / 2] and scales
  * [n_groups][n_out][k_dim / 32] stand for; a, a_rows, offsets, out, the types and the limits
- * are those of moe_grouped_mm, k_dim a multiple of 32. Products of the weights with a are
+ * are those of moe_grouped_mm (with n_groups (rows / 64 + 1) (max(n_out, k_dim) / 16 + 1)
+ * below 2^31), k_dim a multiple of 32. Products of the weights with a are
  * exact, sums in float32. Any number of rows is taken, but every 16 rows of an expert read
  * its weights again: from about 64 rows an expert, moe_weights4_unpack and moe_grouped_mm
  * take less time. No workspace.

@@ -767,14 +767,15 @@ moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_
 // Grouped products. Sizes keep a tile's byte offsets in 32 bits (256 rows of 2^20 + row
 // spacing), row numbers in 31.
 static moe_status check_mm(int32_t dtype, int32_t out_dtype, int32_t groups, int32_t n_out, int32_t k_dim,
-                           int64_t rows, const int32_t* offsets) {
+                           int64_t rows, const int32_t* offsets, int tile = 64) {
   if (!row_dtype(dtype) || !row_dtype(out_dtype) || groups < 1 || n_out < 8 || n_out % 8 || k_dim < 8 || k_dim % 8 ||
       rows < 0 || (!offsets && groups != 1))
     return MOE_ERR_ARG;
   if (groups > MOE_MAX_EXPERTS || n_out > MOE_MM_MAX_DIM || k_dim > MOE_MM_MAX_DIM || rows >= (int64_t(1) << 31) - 512)
     return MOE_ERR_UNSUPPORTED;
-  // tiles are counted in 31 bits, whatever the offsets hold (each group all rows)
-  if (groups * (rows / 64 + 1) * (std::max(n_out, k_dim) / 64 + 1) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  // tiles (64 rows x tile columns at the least) are counted in 31 bits, whatever the offsets
+  // hold (each group all rows)
+  if (groups * (rows / 64 + 1) * (std::max(n_out, k_dim) / tile + 1) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   return maybe(offsets);
 }
 // A matrix of `cols` columns whose rows are ld elements apart.
@@ -888,7 +889,7 @@ moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_
                              const uint8_t* codes1, const uint8_t* scales1, int32_t out_dtype, void* out, int64_t ldo,
                              moe_stream stream) {
   if (op != MOE_GEMM_GATE_UP && op != MOE_GEMM_DOWN) return MOE_ERR_ARG;
-  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets, 16));
   if (k_dim % 32) return MOE_ERR_ARG;
   MOE_TRY(check_mm_a(a, lda, k_dim, a_rows, a_nrows, dtype, rows));
   MOE_TRY(need(codes0));

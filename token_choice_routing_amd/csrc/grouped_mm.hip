@@ -7,6 +7,7 @@
 //   weight gradient  dW[e] = add[e] + sum_p dy[p] a[src(p)]^T   reduces over the rows of e
 // and the product with 4-bit weights (weights4.hpp), plain or as silu(W0 a) * (W1 a).
 #include <algorithm>
+#include <cstdlib>
 
 #include "grouped_mm.hpp"
 #include "rows.hpp"
@@ -116,7 +117,12 @@ __global__ void __launch_bounds__(256) grouped_mm_kernel(GroupedMm g) {
 }  // namespace
 
 hipError_t launch_grouped_mm(const GroupedMm& g, int num_cus, hipStream_t s) {
-  if (g.dtype != MOE_F32 && g.form <= kMmWgrad) return launch_grouped_mm16(g, num_cus, s);
+  if (g.form == kMm4 || g.form == kMm4Swiglu) return launch_grouped_mm_few(g, num_cus, s);
+  if (g.dtype != MOE_F32) {
+    const char* v = getenv("FEW");
+    if (g.form == kMm && v && atoi(v)) return launch_grouped_mm_few(g, num_cus, s);
+    return launch_grouped_mm16(g, num_cus, s);
+  }
   const int I = g.form == kMmWgrad ? g.n_out : 0;
   const int J = g.form == kMmDgrad || g.form == kMmWgrad ? g.k_dim : g.n_out;
   const int64_t nt = (J + kT - 1) / kT;

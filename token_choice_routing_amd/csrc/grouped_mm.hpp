@@ -25,24 +25,24 @@ __device__ __forceinline__ int build_segments(Segments& sg, const int32_t* offse
                                               int nt, int fixed) {
   if (threadIdx.x < kWave) {
     const int lane = threadIdx.x;
-    constexpr int kPer = (kMmGroups + kWave) / kWave;
+    constexpr int kPer = (kMmGroups + 1) / kWave;
+    int32_t off[kPer + 1];  // all loads first
+#pragma unroll
+    for (int q = 0; q <= kPer; ++q) off[q] = offsets ? offsets[min(lane * kPer + q, groups)] : 0;
     int cnt[kPer], local = 0;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int e = lane * kPer + q;
-      int64_t a = 0, b = 0;
+      int a = 0, len = 0;
       if (e < groups) {
-        b = rows;
+        len = (int)rows;
         if (offsets) {
-          a = min<int64_t>(max<int64_t>(offsets[e], 0), rows);
-          b = min<int64_t>(max<int64_t>(offsets[e + 1], a), rows);
+          a = min(max(off[q], 0), (int)rows);
+          len = min(max(off[q + 1], a), (int)rows) - a;
         }
       }
-      const int len = (int)(b - a);
-      if (e <= kMmGroups) {
-        sg.start[e] = (int)a;
-        sg.len[e] = len;
-      }
+      sg.start[e] = a;
+      sg.len[e] = len;
       cnt[q] = e < groups ? ((fixed > 0 ? fixed : len) + bm - 1) / bm * nt : 0;
       local += cnt[q];
     }
@@ -55,8 +55,7 @@ __device__ __forceinline__ int build_segments(Segments& sg, const int32_t* offse
     int run = incl - local;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
-      const int e = lane * kPer + q;
-      if (e <= kMmGroups) sg.prefix[e] = run;
+      sg.prefix[lane * kPer + q] = run;
       run += cnt[q];
     }
   }

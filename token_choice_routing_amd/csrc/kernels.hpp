@@ -334,6 +334,8 @@ struct GroupedMm {
 hipError_t launch_grouped_mm(const GroupedMm& g, int num_cus, hipStream_t s);
 hipError_t launch_grouped_mm16(const GroupedMm& g, int num_cus, hipStream_t s);  // 16-bit dtype, 16-bit weights
 
+hipError_t launch_grouped_mm_few(const GroupedMm& g, int num_cus, hipStream_t s);  // 16-bit product, or 4-bit weights
+
 // 4-bit weights (weights4.hip): blocks of 32 elements.
 hipError_t launch_weights4_pack(int dtype, const void* w, int64_t blocks, void* codes, void* scales, hipStream_t s);
 hipError_t launch_weights4_unpack(int dtype, const void* codes, const void* scales, int64_t blocks, void* out,

@@ -19,4 +19,23 @@ __device__ __forceinline__ float weight4(const uint8_t* codes, const uint8_t* sc
   return q & 8u ? -w : w;
 }
 
+// Eight weights as bf16 (exact) from a dword of codes and the scale byte: the hardware's
+// conversion, which multiplies by the power of two that the float's exponent names; 255 << 23
+// gives NaN for every code, 0 stands for 2^-127.
+__device__ __forceinline__ bf16x8_t weights4_bf16(uint32_t codes, uint32_t scale) {
+  bf16x8_t v = {};
+#if defined(__HIP_DEVICE_COMPILE__)
+  const float s = __uint_as_float(scale << 23);
+  const auto a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 0);
+  const auto b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 1);
+  const auto c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 2);
+  const auto d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(codes, s, 3);
+  v = bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+#else
+  (void)codes;
+  (void)scale;
+#endif
+  return v;
+}
+
 }  // namespace moe
