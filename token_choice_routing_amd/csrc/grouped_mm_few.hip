@@ -1,8 +1,9 @@
 // Grouped products for the few rows of a decode step: 16-bit weights, or 4-bit ones
 // (weights4.hpp), plain or as silu(W0 a) * (W1 a). What bounds them is the bytes of the chosen
 // experts' weights, read once here and straight into registers: an item is one expert's 32
-// weight rows (16 of each matrix for gate/up) times up to 64 of its rows, the four wavefronts
-// of a workgroup take a quarter of the reduction each and add their sums in LDS in order.
+// weight rows (16 of each matrix for gate/up) times up to 16 or 64 of its rows. It belongs to one
+// wavefront, or to the four of a workgroup, which take a quarter of the reduction each and add
+// their sums in LDS in order.
 #include <algorithm>
 
 #include "grouped_mm.hpp"
@@ -13,7 +14,7 @@ namespace moe {
 
 namespace {
 
-constexpr int kFewRows = 64, kChunk = 128;  // rows an item; reduction steps a wavefront takes at a time
+constexpr int kChunk = 128;  // elements of the reduction that a wavefront takes at a time
 
 // Eight consecutive elements of a as loaded, and as N bf16 parts whose sum they are: 8
 // significant bits each (1 part for bf16, 2 for half, 3 for float32; cut off, not rounded, so
@@ -133,106 +134,97 @@ __device__ __forceinline__ f32x4_t mfma_few(bf16x8_t w, bf16x8_t a, f32x4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, a, c, 0, 0, 0);
 }
 
-template <typename T, bool W4, bool SWIGLU>
+// KS wavefronts of the workgroup's four share an item's reduction; 4 / KS items run side by
+// side, of neighbouring columns.
+template <typename T, bool W4, bool SWIGLU, int KS, int MT>
 __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
-  constexpr int U = W4 ? (sizeof(T) == 4 ? 2 : 4) : 2;  // chunks in flight
+  constexpr int kRows = 16 * MT;
   constexpr int NP = W4 ? Parts<T>::N : 1;
+  constexpr int OC = SWIGLU ? 16 : 32, WC = OC * (4 / KS);  // output columns of an item, of the workgroup
   __shared__ Segments sg;
-  __shared__ f32x4_t red[4][kFewRows / 16 * 2][kWave];
-  constexpr int OC = SWIGLU ? 16 : 32;  // output columns an item
-  const int nt = (g.n_out + OC - 1) / OC;
-  const int total = build_segments(sg, g.offsets, g.groups, g.rows, kFewRows, nt, 0);
+  __shared__ f32x4_t red[KS > 1 ? 4 : 1][KS > 1 ? MT * 2 : 1][kWave];
+  const int nt = (g.n_out + WC - 1) / WC;
+  const int total = build_segments(sg, g.offsets, g.groups, g.rows, kRows, nt, 0);
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int l16 = lane & 15, j = lane >> 4;
-  const int K = g.k_dim, chunks = (K + kChunk - 1) / kChunk;
-  const int c0 = chunks * wave / 4, c1 = chunks * (wave + 1) / 4;
+  const int ks = wave % KS, K = g.k_dim, chunks = (K + kChunk - 1) / kChunk;
+  const int c0 = chunks * ks / KS, c1 = chunks * (ks + 1) / KS;
   for (int it = blockIdx.x; it < total; it += gridDim.x) {
     const int e = segment_of(sg, g.groups, it);
-    const int mt = (sg.len[e] + kFewRows - 1) / kFewRows, local = it - sg.prefix[e];
-    const int n0 = local / mt * OC, r0 = sg.start[e] + local % mt * kFewRows;
-    const int rows = __builtin_amdgcn_readfirstlane(min(kFewRows, sg.start[e] + sg.len[e] - r0));
+    const int mt = (sg.len[e] + kRows - 1) / kRows, local = it - sg.prefix[e];
+    const int n0 = local / mt * WC + wave / KS * OC, r0 = sg.start[e] + local % mt * kRows;
+    const int rows = __builtin_amdgcn_readfirstlane(min(kRows, sg.start[e] + sg.len[e] - r0));
     Weights<T, W4> base[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b)
       base[b].at(g, SWIGLU ? b : 0, (int64_t)e * g.n_out + min(n0 + (SWIGLU ? 0 : 16 * b) + l16, g.n_out - 1));
-    auto item = [&](auto tiles) __attribute__((always_inline)) {
-      constexpr int MT = decltype(tiles)::value;
+    {
       f32x4_t acc[MT][2];
       const T* arow[MT];
 #pragma unroll
+      for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4_t{0, 0, 0, 0};
+      // the element that a lane's step i of chunk c begins at, in the weights' order
+      auto col = [&](int c, int i) { return c * kChunk + (W4 ? 32 * j + 8 * i : 32 * i + 8 * j); };
+      struct Set {  // a chunk in registers; two in turn
+        Weights<T, W4> w[2];
+        Parts<T> a[4];
+      };
+      auto load_rows = [&](Set& s, int m, int c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s.a[i].load(arow[m] + (col(c, i) < K ? col(c, i) : 0));
+      };
+      auto load = [&](Set& s, int c) __attribute__((always_inline)) {
+        if (c >= c1) return;
+#pragma unroll
+        for (int b = 0; b < 2; ++b) s.w[b].load(base[b], c, j, K);
+        if (MT == 1) load_rows(s, 0, c);
+      };
+      Set s0, s1;
+      auto multiply = [&](Set& s, int c) __attribute__((always_inline)) {
+        if (c >= c1) return;
+        bf16x8_t wf[4][2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) wf[i][b] = s.w[b].step(i, col(c, i) < K);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if (MT > 1 && 16 * m >= rows) break;
+          if (MT > 1) load_rows(s, m, c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s.a[i].keep(col(c, i) < K);
+            bf16x8_t p[NP];
+            if constexpr (W4) s.a[i].split(p);
+            else p[0] = __builtin_bit_cast(bf16x8_t, s.a[i].v);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int q = 0; q < NP; ++q) acc[m][b] = mfma_few<T, W4>(wf[i][b], p[NP - 1 - q], acc[m][b]);
+          }
+        }
+      };
+      // (the weights of the first chunk are on their way before the rows' numbers are read)
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        if (c0 < c1) s0.w[b].load(base[b], c0, j, K);
+#pragma unroll
       for (int m = 0; m < MT; ++m) {
-        acc[m][0] = acc[m][1] = f32x4_t{0, 0, 0, 0};
         int64_t row = r0 + min(16 * m + l16, rows - 1);
         if (g.a_rows) row = min<int64_t>(max<int64_t>(g.a_rows[row], 0), g.a_nrows - 1);
         arow[m] = static_cast<const T*>(g.a) + row * g.lda;
       }
-      for (int c = c0; c < c1; c += U) {
-        Weights<T, W4> w[U][2];
-        Parts<T> a[MT == 1 ? U : 1][4];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int cu = min(c + u, c1 - 1);
-#pragma unroll
-          for (int b = 0; b < 2; ++b) w[u][b].load(base[b], cu, j, K);
-        }
-        // element order of a chunk's step i: as the weights'
-        auto col = [&](int cu, int i) { return cu * kChunk + (W4 ? 32 * j + 8 * i : 32 * i + 8 * j); };
-        auto load = [&](Parts<T>(&x)[4], const T* p, int cu) __attribute__((always_inline)) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[i].load(p + (col(cu, i) < K ? col(cu, i) : 0));
-        };
-        if (MT == 1) {
-#pragma unroll
-          for (int u = 0; u < U; ++u) load(a[u], arow[0], min(c + u, c1 - 1));
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int cu = c + u;
-          if (cu >= c1) break;
-          bf16x8_t wf[4][2];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int b = 0; b < 2; ++b) wf[i][b] = w[u][b].step(i, col(cu, i) < K);
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if (MT > 1 && 16 * m >= rows) break;
-            Parts<T>(&x)[4] = a[MT == 1 ? u : 0];
-            if (MT > 1) load(x, arow[m], cu);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              x[i].keep(col(cu, i) < K);
-              bf16x8_t p[NP];
-              if constexpr (W4) x[i].split(p);
-              else p[0] = __builtin_bit_cast(bf16x8_t, x[i].v);
-#pragma unroll
-              for (int b = 0; b < 2; ++b)
-#pragma unroll
-                for (int q = 0; q < NP; ++q) acc[m][b] = mfma_few<T, W4>(wf[i][b], p[NP - 1 - q], acc[m][b]);
-            }
-          }
-        }
+      if (MT == 1 && c0 < c1) load_rows(s0, 0, c0);
+      load(s1, c0 + 1);
+      for (int c = c0; c < c1; c += 2) {
+        multiply(s0, c);
+        load(s0, c + 2);
+        multiply(s1, c + 1);
+        load(s1, c + 3);
       }
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int b = 0; b < 2; ++b) red[wave][2 * m + b][lane] = acc[m][b];
-      __syncthreads();
       // lane: row l16 of 16, four columns 4 j .. of 16
-      auto sum = [&](int q) __attribute__((always_inline)) {
-        return (red[0][q][lane] + red[1][q][lane]) + (red[2][q][lane] + red[3][q][lane]);
-      };
-#pragma unroll
-      for (int q = 0; q < (SWIGLU ? MT : 2 * MT); ++q) {
-        if ((q & 3) != wave) continue;
-        const int r = 16 * (SWIGLU ? q : q / 2) + l16, n = n0 + (SWIGLU ? 0 : 16 * (q & 1)) + 4 * j;
-        f32x4_t v = sum(SWIGLU ? 2 * q : q);
-        if constexpr (SWIGLU) {
-          const f32x4_t up = sum(2 * q + 1);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
-        }
-        if (r >= rows || n >= g.n_out) continue;
+      auto store = [&](int r, int n, const f32x4_t& v) __attribute__((always_inline)) {
+        if (r >= rows || n >= g.n_out) return;
         const int64_t at = (int64_t)(r0 + r) * g.ldo + n;
         if (g.out_dtype == MOE_F32)
           *reinterpret_cast<f32x4_t*>(static_cast<float*>(g.out) + at) = v;
@@ -242,32 +234,77 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
         else
           *reinterpret_cast<u32x2_t*>(static_cast<uint16_t*>(g.out) + at) =
               u32x2_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])};
+      };
+      auto act = [&](f32x4_t v, const f32x4_t& up) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = silu(v[i]) * up[i];
+        return v;
+      };
+      if constexpr (KS == 1) {
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int r = 16 * m + l16, n = n0 + 4 * j;
+          if constexpr (SWIGLU) {
+            store(r, n, act(acc[m][0], acc[m][1]));
+          } else {
+            store(r, n, acc[m][0]);
+            store(r, n + 16, acc[m][1]);
+          }
+        }
+      } else {
+        static_assert(KS == 4, "the sums below are of four wavefronts");
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) red[wave][2 * m + b][lane] = acc[m][b];
+        __syncthreads();
+        auto sum = [&](int q) __attribute__((always_inline)) {
+          return (red[0][q][lane] + red[1][q][lane]) + (red[2][q][lane] + red[3][q][lane]);
+        };
+#pragma unroll
+        for (int q = 0; q < (SWIGLU ? MT : 2 * MT); ++q) {
+          if ((q & 3) != wave) continue;
+          if constexpr (SWIGLU) store(16 * q + l16, n0 + 4 * j, act(sum(2 * q), sum(2 * q + 1)));
+          else store(16 * (q / 2) + l16, n0 + 16 * (q & 1) + 4 * j, sum(q));
+        }
+        __syncthreads();  // before the next item's sums
       }
-      __syncthreads();  // before the next item's sums
-    };
-    if (rows <= 16) item(std::integral_constant<int, 1>{});
-    else item(std::integral_constant<int, kFewRows / 16>{});
+    }
   }
 }
 
 }  // namespace
 
+// Rules (us at 64 experts, n 2048, k 1536, bf16): a wavefront takes the whole reduction where
+// there are items for most of them (64 rows: 33 against 40 with a quarter each; 2 rows of two
+// experts, n 1536, k 2048: 13 against 8); 64 rows an item where an expert has more than 16
+// (64 rows: 41 against 37 with 16; 1024 rows: 47 and 46; with 32 rows an expert 69 for 64, as
+// 16 read and convert every weight twice).
 hipError_t launch_grouped_mm_few(const GroupedMm& g, int num_cus, hipStream_t s) {
-  const bool w4 = g.form != kMm, swiglu = g.form == kMm4Swiglu;
-  const int64_t nt = (g.n_out + (swiglu ? 15 : 31)) / (swiglu ? 16 : 32);
-  const int64_t items = (g.rows / kFewRows + std::min<int64_t>(g.groups, g.rows)) * nt;
+  const bool swiglu = g.form == kMm4Swiglu, tall = g.rows > 16 * (int64_t)g.groups;
+  const int oc = swiglu ? 16 : 32;
+  const int64_t segments = g.rows / (tall ? 64 : 16) + std::min<int64_t>(g.groups, g.rows);
+  const bool whole = segments * ((g.n_out + oc - 1) / oc) >= 4 * num_cus;
+  const int wc = whole ? 4 * oc : oc;
+  const int64_t items = segments * ((g.n_out + wc - 1) / wc);
   const unsigned blocks = (unsigned)std::min<int64_t>(items, 4 * num_cus);
+  auto go = [&](auto kernel) {
+    kernel<<<blocks, 256, 0, s>>>(g);
+    return hipGetLastError();
+  };
   return with_rows(g.dtype, [&](auto* t) {
     typedef std::remove_pointer_t<decltype(t)> T;
-    if (!w4) {
-      if constexpr (sizeof(T) == 2) grouped_mm_few_kernel<T, false, false><<<blocks, 256, 0, s>>>(g);
-      else return hipErrorInvalidValue;
-    } else if (swiglu) {
-      grouped_mm_few_kernel<T, true, true><<<blocks, 256, 0, s>>>(g);
-    } else {
-      grouped_mm_few_kernel<T, true, false><<<blocks, 256, 0, s>>>(g);
+    if (g.form == kMm) {
+      if constexpr (sizeof(T) == 2)
+        return go(whole ? grouped_mm_few_kernel<T, false, false, 1, 1> : grouped_mm_few_kernel<T, false, false, 4, 1>);
+      return hipErrorInvalidValue;
     }
-    return hipGetLastError();
+    auto four_bit = [&](auto act) {
+      constexpr bool S = decltype(act)::value;
+      if (tall) return go(whole ? grouped_mm_few_kernel<T, true, S, 1, 4> : grouped_mm_few_kernel<T, true, S, 4, 4>);
+      return go(whole ? grouped_mm_few_kernel<T, true, S, 1, 1> : grouped_mm_few_kernel<T, true, S, 4, 1>);
+    };
+    return swiglu ? four_bit(std::true_type{}) : four_bit(std::false_type{});
   });
 }
 
