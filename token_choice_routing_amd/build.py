@@ -19,7 +19,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libmoe_mi355x.so")
 SOURCES = ["api.hip", "route.hip", "permute.hip", "ffn.hip", "combine.hip", "aux.hip", "backward.hip", "validate.hip",
-           "dispatch_grad.hip", "act8.hip", "grouped_mm.hip", "grouped_mm16.hip",
+           "dispatch_grad.hip", "act8.hip", "grouped_mm_tiles.hip",
            "grouped_mm_few.hip", "weights4.hip"]
 MARSHAL = os.path.join(HERE, "_marshal.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

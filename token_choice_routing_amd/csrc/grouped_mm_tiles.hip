@@ -1,5 +1,12 @@
-// Grouped products of 16-bit rows and weights on the matrix cores (forms as in
-// grouped_mm.hip): tiles of BM x BN outputs, the reduction 32 at a time.
+// Products of rows in expert order with their expert's weights, over segments of any
+// length (the grouped GEMM of the paper review "Improving MoE Compute Efficiency by
+// Composing Weight and Data Sparsity", section 3 "implementation", as plain products with
+// gradients, for experts of one's own):
+//   product          out[p] = W[e] a[src(p)]           reduces over k_dim
+//   data gradient    da[p] = W[e]^T dy[p]              reduces over n_out
+//   weight gradient  dW[e] = add[e] + sum_p dy[p] a[src(p)]^T   reduces over the rows of e
+// Each is C[i][j] = sum_k A[i][k] B[j][k] on the matrix cores, in tiles of BM x BN outputs and
+// 64 bytes of a row (32 16-bit elements or 16 float32 ones) of the reduction at a time.
 #include <algorithm>
 
 #include "grouped_mm.hpp"
@@ -9,7 +16,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kBK = 32;
 constexpr uint32_t kPast = 0xfffffff0u;     // byte offset past every resource: reads zero, touches nothing
 constexpr uint32_t kRecords = 0xffffff00u;  // (lanes that read anything are bounded by their own tests)
 
@@ -17,13 +23,23 @@ constexpr int kBand = 8;  // row tiles
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 
+// One step of a 32 x 32 block: 16 bytes of a J row and an I row a lane, lane half h holding the
+// step's elements of its half. 16-bit: one product 16 deep. float32: four, 2 deep, element s of
+// both halves in product s.
 template <typename T>
-__device__ __forceinline__ f32x16_t mfma16(bf16x8_t j, bf16x8_t i, f32x16_t c) {
-  if constexpr (std::is_same<T, bf16_t>::value)
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(j, i, c, 0, 0, 0);
-  else
+__device__ __forceinline__ f32x16_t multiply_block(u32x4_t j, u32x4_t i, f32x16_t c) {
+  if constexpr (std::is_same<T, float>::value) {
+    const f32x4_t x = __builtin_bit_cast(f32x4_t, j), y = __builtin_bit_cast(f32x4_t, i);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f32_32x32x2f32(x[s], y[s], c, 0, 0, 0);
+    return c;
+  } else if constexpr (std::is_same<T, bf16_t>::value) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, j), __builtin_bit_cast(bf16x8_t, i), c,
+                                                   0, 0, 0);
+  } else {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, j), __builtin_bit_cast(f16x8_t, i), c, 0,
                                                   0, 0);
+  }
 }
 
 // A 4-element column of a K-major stage by the transposing LDS read: within each 16-lane
@@ -50,12 +66,13 @@ __device__ __forceinline__ void deal(int n, F&& f) {
 
 template <typename T, int FORM, int BM, int BN, int WM, int WN, int S>
 __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
-grouped_mm16_kernel(GroupedMm g) {
+grouped_mm_tiles_kernel(GroupedMm g) {
+  constexpr int ES = sizeof(T), EC = 16 / ES, kBK = 64 / ES;  // bytes an element; elements of 16 bytes, of a stage's row
   constexpr int NW = WM * WN, FM = BM / WM / 32, FN = BN / WN / 32;
   constexpr bool KI = FORM == kMmWgrad, KJ = FORM != kMm;  // K-major operands (the reduction runs over their rows)
   constexpr int PI = BM / 16 / NW, PJ = BN / 16 / NW;      // 1 KB pieces of a stage that a wavefront loads
   constexpr int PL = PI + PJ;
-  constexpr int STAGE = (BM + BN) * kBK * 2;               // bytes
+  constexpr int STAGE = (BM + BN) * 64;                    // bytes
   __shared__ Segments sg;
   extern __shared__ __attribute__((aligned(16))) char smem[];  // [S][I region, J region]
   const int I = KI ? g.n_out : 0, J = FORM == kMm ? g.n_out : g.k_dim;
@@ -93,14 +110,17 @@ grouped_mm16_kernel(GroupedMm g) {
     return w;
   };
 
-  // This lane's share of a piece. Row-major: 16 rows of 32, the lane's 16-byte chunk lc of
-  // row lane / 4 (chunks XOR-ed with (row / 4) % 4 against bank conflicts). K-major: 512 / B
-  // K rows of B columns, 64-byte groups XOR-ed with the K row.
+  // This lane's share of a piece. Row-major: 16 rows of 64 bytes, the lane's 16-byte chunk lc of
+  // row lane / 4 (chunks XOR-ed with (row / 4) % 4 against bank conflicts). K-major: K rows of B
+  // columns, 32-column groups XOR-ed with the K row (16-bit, whose reads take four K rows at
+  // once) or its half of the stage (float32, whose reads take one of each half).
   const int lc = (lane & 3) ^ (lane >> 4);
-  auto krow = [&](int piece, int B) __attribute__((always_inline)) { return piece * (512 / B) + lane / (B / 8); };
-  auto kcol = [&](int kr, int B) __attribute__((always_inline)) {
-    const int p = lane % (B / 8);
-    return ((p & 3) | (((p >> 2) ^ (kr & 3)) << 2)) * 8;
+  auto krow = [&](int piece, int B) { return piece * (1024 / (B * ES)) + lane / (B * ES / 16); };
+  auto kswap = [&](int kr) { return ES == 2 ? kr & 3 : (kr >> 3) & 1; };
+  auto kcol = [&](int kr, int B) {
+    constexpr int GC = 32 / EC;  // chunks of a 32-column group
+    const int p = lane % (B * ES / 16);
+    return (p % GC + ((p / GC) ^ kswap(kr)) * GC) * EC;
   };
 
   // ---- the stream of K tiles, S ahead of the products, item after item
@@ -109,13 +129,13 @@ grouped_mm16_kernel(GroupedMm g) {
   uint32_t ioff[PI], joff[PJ];
   int lit = slot, lkt = 0, lnk = 0, lklen = 0, lstart = 0;
   int64_t istep = 0, jstep = 0;
-  const uint32_t lda2 = (uint32_t)g.lda * 2;
+  const uint32_t lda_bytes = (uint32_t)g.lda * ES;
   // Gathered rows of the reduction: the rows that the wavefront's pieces of
   // the next K tile hold (the same in every lane, read as scalars a tile ahead: vector loads
   // return in order, so one would wait for every tile in flight).
-  constexpr int KPP = KJ ? 512 / BN : 1;
+  constexpr int KPP = KJ ? 1024 / (BN * ES) : 1;
   int32_t idx[PJ][KPP];
-  const int last_row = (int)g.a_nrows - 1;  // ((a_nrows + 1) lda 2 bytes fit in 32 bits)
+  const int last_row = (int)g.a_nrows - 1;  // ((a_nrows + 1) rows fit in 32 bits)
   typedef const __attribute__((address_space(4))) int32_t* scalar_rows;
   const scalar_rows a_rows = (scalar_rows)(uintptr_t)g.a_rows;
   auto fetch_rows = [&]() __attribute__((always_inline)) {
@@ -159,12 +179,12 @@ grouped_mm16_kernel(GroupedMm g) {
       for (int p = 0; p < PI; ++p) {
         if constexpr (KI) {
           const int kr = krow(wave + NW * p, BM), c = kcol(kr, BM);
-          ioff[p] = c < w.iv ? (uint32_t)(kr * ild + c) * 2u : kPast;
+          ioff[p] = c < w.iv ? (uint32_t)(kr * ild + c) * ES : kPast;
         } else {
           const int r = 16 * (wave + NW * p) + (lane >> 2);
           int64_t row = r;
           if (gather) row = min<int64_t>(max<int64_t>(nrow[p], 0), g.a_nrows - 1);
-          ioff[p] = r < w.iv ? (uint32_t)(row * ild + lc * 8) * 2u : kPast;
+          ioff[p] = r < w.iv ? (uint32_t)(row * ild + lc * EC) * ES : kPast;
         }
       }
       const T* jbase;
@@ -179,10 +199,10 @@ grouped_mm16_kernel(GroupedMm g) {
         if constexpr (KJ) {
           const int kr = krow(wave + NW * p, BN), c = kcol(kr, BN);
           const bool rowless = FORM == kMmWgrad && g.a_rows;  // the row is added at each tile
-          joff[p] = c < w.jv ? (uint32_t)((rowless ? 0 : kr * jld) + c) * 2u : kPast;
+          joff[p] = c < w.jv ? (uint32_t)((rowless ? 0 : kr * jld) + c) * ES : kPast;
         } else {
           const int r = 16 * (wave + NW * p) + (lane >> 2);
-          joff[p] = r < w.jv ? (uint32_t)(r * jld + lc * 8) * 2u : kPast;
+          joff[p] = r < w.jv ? (uint32_t)(r * jld + lc * EC) * ES : kPast;
         }
       }
       if (FORM == kMmWgrad && g.a_rows) fetch_rows();
@@ -199,22 +219,22 @@ grouped_mm16_kernel(GroupedMm g) {
 #pragma unroll
     for (int p = 0; p < PI; ++p) {
       const int piece = wave + NW * p;
-      const int k = k0 + (KI ? krow(piece, BM) : lc * 8);
+      const int k = k0 + (KI ? krow(piece, BM) : lc * EC);
       buffer_load_lds16(ri, whole || k < lklen ? ioff[p] : kPast, reinterpret_cast<bf16_t*>(stage + piece * 1024));
     }
 #pragma unroll
     for (int p = 0; p < PJ; ++p) {
       const int piece = wave + NW * p;
-      const int k = k0 + (KJ ? krow(piece, BN) : lc * 8);
+      const int k = k0 + (KJ ? krow(piece, BN) : lc * EC);
       uint32_t off = joff[p];
       if (FORM == kMmWgrad && g.a_rows) {
         int row = idx[p][0];
 #pragma unroll
-        for (int q = 1; q < KPP; ++q) row = lane / (BN / 8) >= q ? idx[p][q] : row;
-        off = off == kPast ? kPast : off + (uint32_t)min(max(row, 0), last_row) * lda2;
+        for (int q = 1; q < KPP; ++q) row = lane / (BN * ES / 16) >= q ? idx[p][q] : row;
+        off = off == kPast ? kPast : off + (uint32_t)min(max(row, 0), last_row) * lda_bytes;
       }
       buffer_load_lds16(rj, whole || k < lklen ? off : kPast,
-                        reinterpret_cast<bf16_t*>(stage + BM * kBK * 2 + piece * 1024));
+                        reinterpret_cast<bf16_t*>(stage + BM * 64 + piece * 1024));
     }
     isrc = uniform_ptr(isrc + istep);
     jsrc = uniform_ptr(jsrc + jstep);
@@ -230,35 +250,45 @@ grouped_mm16_kernel(GroupedMm g) {
     }
   };
 
-  // ---- fragments: per 16-wide K step FN J blocks and FM I blocks of 32
+  // ---- fragments: per half of a stage's K FN J blocks and FM I blocks of 32, 16 bytes a lane.
+  // Row-major: chunk 2 ks + h (16-bit) or ks + 2 h (float32) of the lane's row for half h of the
+  // lanes. K-major, 16-bit: two transposing reads; float32: an element of each of four K rows.
+  auto chunk_of = [&](int ks) { return ES == 2 ? 2 * ks + half : ks + 2 * half; };
   uint32_t iaddr[KI ? FM : 2], jaddr[KJ ? FN : 2];
   {
     const int s16 = lane & 15;
-    const int kl = 8 * half + (s16 >> 2), nl = 16 * ((lane >> 4) & 1) + 4 * (s16 & 3);
+    const int kl = 8 * half + (ES == 2 ? s16 >> 2 : 0), nl = ES == 2 ? 16 * ((lane >> 4) & 1) + 4 * (s16 & 3) : l32;
     if constexpr (KI) {
 #pragma unroll
-      for (int b = 0; b < FM; ++b) iaddr[b] = (uint32_t)(kl * BM + (((b * WM + wm) ^ (kl & 3)) * 32) + nl) * 2;
+      for (int b = 0; b < FM; ++b) iaddr[b] = (uint32_t)(kl * BM + ((b * WM + wm) ^ kswap(kl)) * 32 + nl) * ES;
     } else {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        iaddr[ks] = (uint32_t)((wm * 32 + l32) * kBK + (((2 * ks + half) ^ ((l32 >> 2) & 3)) << 3)) * 2;
+        iaddr[ks] = (uint32_t)((wm * 32 + l32) * 64 + ((chunk_of(ks) ^ ((l32 >> 2) & 3)) << 4));
     }
     if constexpr (KJ) {
 #pragma unroll
       for (int b = 0; b < FN; ++b)
-        jaddr[b] = (uint32_t)(BM * kBK + kl * BN + (((wn * FN + b) ^ (kl & 3)) * 32) + nl) * 2;
+        jaddr[b] = (uint32_t)(BM * 64 + (kl * BN + ((wn * FN + b) ^ kswap(kl)) * 32 + nl) * ES);
     } else {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks)
-        jaddr[ks] = (uint32_t)(BM * kBK + (wn * FN * 32 + l32) * kBK + (((2 * ks + half) ^ ((l32 >> 2) & 3)) << 3)) * 2;
+        jaddr[ks] = (uint32_t)(BM * 64 + (wn * FN * 32 + l32) * 64 + ((chunk_of(ks) ^ ((l32 >> 2) & 3)) << 4));
     }
   }
   struct Frags {
-    bf16x8_t j[FN], i[FM];
+    u32x4_t j[FN], i[FM];
   };
   auto column = [&](const char* p, int ks, int B) __attribute__((always_inline)) {
-    const s16x4_t lo = read_tr(p + ks * 16 * B * 2), hi = read_tr(p + (ks * 16 + 4) * B * 2);
-    return __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    if constexpr (ES == 2) {
+      const s16x4_t lo = read_tr(p + ks * 16 * B * 2), hi = read_tr(p + (ks * 16 + 4) * B * 2);
+      return __builtin_bit_cast(u32x4_t, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      u32x4_t v;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) v[s] = *reinterpret_cast<const uint32_t*>(p + (4 * ks + s) * B * 4);
+      return v;
+    }
   };
   auto read = [&](auto blocks, int st, int ks, Frags& f) __attribute__((always_inline)) {
     constexpr int NB = decltype(blocks)::value;
@@ -266,12 +296,12 @@ grouped_mm16_kernel(GroupedMm g) {
 #pragma unroll
     for (int b = 0; b < FN; ++b) {
       if constexpr (KJ) f.j[b] = column(stage + jaddr[b], ks, BN);
-      else f.j[b] = *reinterpret_cast<const bf16x8_t*>(stage + jaddr[ks] + b * 32 * kBK * 2);
+      else f.j[b] = *reinterpret_cast<const u32x4_t*>(stage + jaddr[ks] + b * 32 * 64);
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if constexpr (KI) f.i[b] = column(stage + iaddr[b], ks, BM);
-      else f.i[b] = *reinterpret_cast<const bf16x8_t*>(stage + iaddr[ks] + b * WM * 32 * kBK * 2);
+      else f.i[b] = *reinterpret_cast<const u32x4_t*>(stage + iaddr[ks] + b * WM * 32 * 64);
     }
   };
 
@@ -283,6 +313,7 @@ grouped_mm16_kernel(GroupedMm g) {
     return KI ? ((int64_t)w.e * g.n_out + w.i0) * g.k_dim + w.j0 : (int64_t)(w.start + w.i0) * g.ldo + w.j0;
   };
   auto piece_at = [&](char* stage, int i) __attribute__((always_inline)) {
+    if (PL < 4) return smem + S * STAGE + (4 * wave + i) * 1024;  // (too few pieces: LDS of its own)
     return stage + (i < PI ? wave + NW * i : BM / 16 + wave + NW * (i - PI)) * 1024;
   };
   // OT: the output type (float: 32-column blocks; uint32_t: 16-bit ones, 64 columns at a time
@@ -290,7 +321,8 @@ grouped_mm16_kernel(GroupedMm g) {
   auto store = [&](auto type, auto added, auto stream, const Item& w, const f32x16_t (&acc)[FN][FM], char* stage) __attribute__((always_inline)) {
     typedef decltype(type) OT;
     constexpr bool ADD = decltype(added)::value, WIDE = std::is_same<OT, float>::value || ADD;
-    constexpr int C = WIDE ? 1 : 2;  // 32-column blocks at a time
+    constexpr int C = WIDE || FN == 1 ? 1 : 2;  // 32-column blocks at a time
+    constexpr int CL = WIDE ? 4 : 8;            // columns a lane reads back
     constexpr int kPolicy = decltype(stream)::value ? 2 : 0;  // nt: not kept in the caches
     const int lane = opaque_v((int)threadIdx.x) & (kWave - 1), half = lane >> 5, l32 = lane & 31;
     const int r8 = lane >> 3, c8 = lane & 7;
@@ -321,14 +353,15 @@ grouped_mm16_kernel(GroupedMm g) {
               *reinterpret_cast<u32x2_t*>(put + (((4 * h + q) ^ (l32 & 7)) << 4) + 8 * half) =
                   u32x2_t{pack(x[0], x[1]), pack(x[2], x[3])};
           }
-        const int c = wn * FN * 32 + f * 32 + 4 * C * c8;
+        const int c = wn * FN * 32 + f * 32 + CL * c8;
+        const bool cols = CL * c8 < 32 * C;  // (half a line of 16-bit outputs where FN is 1)
         u32x4_t x[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const u32x4_t*>(mine[i] + get);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = (b * WM + wm) * 32 + 8 * i + r8;
-          const bool in = r < w.iv && c < w.jv;
+          const bool in = cols && r < w.iv && c < w.jv;
           const uint32_t el = (uint32_t)r * ld + (uint32_t)c;
           if constexpr (ADD) {
             const f32x4_t y =
@@ -408,7 +441,7 @@ grouped_mm16_kernel(GroupedMm g) {
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) acc[j][b] = mfma16<T>(f.j[j], f.i[b], acc[j][b]);
+          for (int b = 0; b < NB; ++b) acc[j][b] = multiply_block<T>(f.j[j], f.i[b], acc[j][b]);
       };
       Frags f0, f1;
       if (NB && nk) read(blocks, st, 0, f0);
@@ -445,7 +478,7 @@ grouped_mm16_kernel(GroupedMm g) {
 
 template <typename T, int BM, int BN, int WM, int WN, int S>
 hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
-  constexpr size_t lds = (size_t)S * (BM + BN) * kBK * 2;
+  constexpr size_t lds = (size_t)S * (BM + BN) * 64 + ((BM + BN) / 16 / (WM * WN) < 4 ? WM * WN * 4096 : 0);
   const int J = g.form == kMm ? g.n_out : g.k_dim;
   const int64_t nt = (J + BN - 1) / BN;
   const int64_t mt = g.form == kMmWgrad ? (int64_t)g.groups * ((g.n_out + BM - 1) / BM) : g.rows / BM + g.groups;
@@ -458,9 +491,9 @@ hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
     return hipGetLastError();
   };
   switch (g.form) {
-    case kMm: return go(grouped_mm16_kernel<T, kMm, BM, BN, WM, WN, S>);
-    case kMmDgrad: return go(grouped_mm16_kernel<T, kMmDgrad, BM, BN, WM, WN, S>);
-    case kMmWgrad: return go(grouped_mm16_kernel<T, kMmWgrad, BM, BN, WM, WN, S>);
+    case kMm: return go(grouped_mm_tiles_kernel<T, kMm, BM, BN, WM, WN, S>);
+    case kMmDgrad: return go(grouped_mm_tiles_kernel<T, kMmDgrad, BM, BN, WM, WN, S>);
+    case kMmWgrad: return go(grouped_mm_tiles_kernel<T, kMmWgrad, BM, BN, WM, WN, S>);
   }
   return hipErrorInvalidValue;
 }
@@ -472,19 +505,34 @@ hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
 //   data gradient 1024 of 8: 29 and 21, 9600 of 64: 97 and 141 (and 73 and 78 at 1024 of 64)
 //   weight gradient 32768 of 8, 1024 x 1024 (128 tiles of 256 x 256): 100 and 80; 16384 of 1, 1536 x
 //   2048: 346 and 177; 16372 of 64, 768 x 1024 (768 tiles): 60 and 103
+// float32: 64 x 64 where 128 x 128 would. us with 128 and 64: 896 rows of 16 experts, 520 x 264: 16
+// and 11, data gradient 27 and 17; 8192 of 8, 768 x 1024: 130 and 128, data gradient 105 and 132;
+// weight gradient 4096 of 1, 1024 x 1024 (64 tiles): 285 and 103; 32970 of 64, 768 x 1024: 420 and 577
 template <typename T>
 hipError_t launch_for(const GroupedMm& g, int num_cus, hipStream_t s) {
-  const int64_t nt = ((g.form == kMm ? g.n_out : g.k_dim) + 255) / 256;
-  const int64_t mt = g.form == kMmWgrad ? (int64_t)g.groups * ((g.n_out + 255) / 256) : g.rows / 256 + g.groups;
-  const bool small = g.form == kMmWgrad ? mt * nt < 2 * num_cus
-                                        : mt * nt < num_cus || (g.form == kMm && g.rows <= 64 * (int64_t)g.groups);
-  return small ? launch_tiles<T, 128, 128, 2, 2, 4>(g, num_cus, s) : launch_tiles<T, 256, 256, 2, 4, 4>(g, num_cus, s);
+  const int J = g.form == kMm ? g.n_out : g.k_dim;
+  auto tiles = [&](int b) {
+    return (g.form == kMmWgrad ? (int64_t)g.groups * ((g.n_out + b - 1) / b) : g.rows / b + g.groups) * ((J + b - 1) / b);
+  };
+  if constexpr (std::is_same<T, float>::value) {
+    const bool small = tiles(128) < num_cus;
+    return small ? launch_tiles<T, 64, 64, 2, 2, 4>(g, num_cus, s) : launch_tiles<T, 128, 128, 2, 2, 4>(g, num_cus, s);
+  } else {
+    const bool small = g.form == kMmWgrad
+                           ? tiles(256) < 2 * num_cus
+                           : tiles(256) < num_cus || (g.form == kMm && g.rows <= 64 * (int64_t)g.groups);
+    return small ? launch_tiles<T, 128, 128, 2, 2, 4>(g, num_cus, s) : launch_tiles<T, 256, 256, 2, 4, 4>(g, num_cus, s);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_grouped_mm16(const GroupedMm& g, int num_cus, hipStream_t s) {
-  return g.dtype == MOE_BF16 ? launch_for<bf16_t>(g, num_cus, s) : launch_for<half_t>(g, num_cus, s);
+hipError_t launch_grouped_mm(const GroupedMm& g, int num_cus, hipStream_t s) {
+  // few rows: 73 us against 80 with 4 rows of each of 64 experts (n 2048, k 1536), 81 and 84
+  // with 16, 111 and 87 with 32; 2 rows of two experts 8 and 18
+  const bool few = g.form == kMm && g.dtype != MOE_F32 && g.rows <= 16 * (int64_t)g.groups;
+  if (few || g.form == kMm4 || g.form == kMm4Swiglu) return launch_grouped_mm_few(g, num_cus, s);
+  return with_rows(g.dtype, [&](auto* t) { return launch_for<std::remove_pointer_t<decltype(t)>>(g, num_cus, s); });
 }
 
 }  // namespace moe

@@ -311,7 +311,8 @@ struct SwigluBwd8Args {
 };
 hipError_t launch_swiglu_bwd8(const SwigluBwd8Args& a, hipStream_t s);
 
-// Products of rows in expert order with their expert's weights (grouped_mm.hip).
+// Products of rows in expert order with their expert's weights (grouped_mm_tiles.hip, and
+// grouped_mm_few.hip for few rows and for 4-bit weights).
 enum { kMm = 0, kMmDgrad = 1, kMmWgrad = 2, kMm4 = 3, kMm4Swiglu = 4 };
 struct GroupedMm {
   int form;
@@ -332,7 +333,6 @@ struct GroupedMm {
   int64_t ldo;              // (weight gradient: dense)
 };
 hipError_t launch_grouped_mm(const GroupedMm& g, int num_cus, hipStream_t s);
-hipError_t launch_grouped_mm16(const GroupedMm& g, int num_cus, hipStream_t s);  // 16-bit dtype, 16-bit weights
 
 hipError_t launch_grouped_mm_few(const GroupedMm& g, int num_cus, hipStream_t s);  // 16-bit product, or 4-bit weights
 
