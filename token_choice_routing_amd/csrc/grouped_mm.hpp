@@ -9,18 +9,22 @@ namespace moe {
 constexpr int kMmGroups = MOE_MAX_EXPERTS;
 static_assert((kMmGroups + 1) % kWave == 0, "segment_of reads whole wavefronts of the table");
 
+constexpr int kTileCost = 256;  // work of a weight gradient's tile beside its rows (its stores), in rows
+
 // Row ranges of the groups and the running count of their output tiles.
 struct Segments {
   int start[kMmGroups + 1];
   int len[kMmGroups + 1];
   int prefix[kMmGroups + 1];  // tiles before group e
+  int64_t cost[kMmGroups + 1];  // weight gradient: work before group e
 };
 
 // Group e's rows are [a, b) with a = clamp(offsets[e], 0, rows), b = clamp(offsets[e + 1], a,
 // rows): inside the buffers whatever the offsets hold. A group has ceil(extent / bm) * nt
 // tiles, extent being its rows, or `fixed` where that is positive (a weight gradient: every
 // group's output has n_out rows). Called by the whole workgroup (at least one wavefront);
-// returns the number of tiles.
+// returns the number of tiles. `fixed` also fills in the work: a tile's is its group's rows and
+// kTileCost more.
 __device__ __forceinline__ int build_segments(Segments& sg, const int32_t* offsets, int groups, int64_t rows, int bm,
                                               int nt, int fixed) {
   if (threadIdx.x < kWave) {
@@ -30,6 +34,7 @@ __device__ __forceinline__ int build_segments(Segments& sg, const int32_t* offse
 #pragma unroll
     for (int q = 0; q <= kPer; ++q) off[q] = offsets ? offsets[min(lane * kPer + q, groups)] : 0;
     int cnt[kPer], local = 0;
+    int64_t work[kPer], lwork = 0;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       const int e = lane * kPer + q;
@@ -45,18 +50,28 @@ __device__ __forceinline__ int build_segments(Segments& sg, const int32_t* offse
       sg.len[e] = len;
       cnt[q] = e < groups ? ((fixed > 0 ? fixed : len) + bm - 1) / bm * nt : 0;
       local += cnt[q];
+      work[q] = (int64_t)cnt[q] * (len + kTileCost);
+      lwork += work[q];
     }
     int incl = local;
+    int64_t iwork = lwork;
 #pragma unroll
     for (int o = 1; o < kWave; o <<= 1) {
       const int v = __shfl_up(incl, o, kWave);
       if (lane >= o) incl += v;
+      if (fixed > 0) {
+        const int64_t x = __shfl_up(iwork, o, kWave);
+        if (lane >= o) iwork += x;
+      }
     }
     int run = incl - local;
+    iwork -= lwork;
 #pragma unroll
     for (int q = 0; q < kPer; ++q) {
       sg.prefix[lane * kPer + q] = run;
       run += cnt[q];
+      if (fixed > 0) sg.cost[lane * kPer + q] = iwork;
+      iwork += work[q];
     }
   }
   __syncthreads();
@@ -75,6 +90,24 @@ __device__ __forceinline__ int segment_of(const Segments& sg, int groups, int t)
     n += __popcll(ballot(e < groups && p <= t));
   }
   return n - 1;
+}
+
+// The first tile of share x of 8 of a weight gradient's work, by every lane of a wavefront: the
+// groups' rows, and with them their tiles' times, differ much.
+__device__ __forceinline__ int work_share(const Segments& sg, int groups, int total, int x) {
+  if (x >= 8) return total;
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t at = sg.cost[groups] / 8 * x;
+  int n = 0;
+#pragma unroll
+  for (int q = 0; q < (kMmGroups + 1) / kWave; ++q) {
+    const int e = q * kWave + lane;
+    const int64_t c = sg.cost[e];
+    n += __popcll(ballot(e < groups && c <= at));
+  }
+  const int e = max(n - 1, 0);
+  const int64_t within = (at - sg.cost[e]) / (sg.len[e] + kTileCost);
+  return min(sg.prefix[e] + (int)within, total);
 }
 
 }  // namespace moe

@@ -82,10 +82,11 @@ grouped_mm_tiles_kernel(GroupedMm g) {
   const int wm = wave / WN, wn = wave % WN;  // (the wavefronts of a SIMD have different rows)
   const int half = lane >> 5, l32 = lane & 31;
 
-  // Tiles (expert, band of row tiles, column tile, row tile), an eighth of the list for each
-  // XCD: the tiles it runs at once share weight panels and row panels in its L2.
+  // Tiles (expert, band of row tiles, column tile, row tile), an eighth of the list (of a weight
+  // gradient's: of the work) for each XCD: the tiles it runs at once share weight panels and row panels in its L2.
   const int xcd = blockIdx.x & 7, slot = blockIdx.x >> 3, per = gridDim.x >> 3;
-  const int first = (int)((int64_t)xcd * total / 8), count = (int)((int64_t)(xcd + 1) * total / 8) - first;
+  const int first = uniform(KI ? work_share(sg, g.groups, total, xcd) : (int)((int64_t)xcd * total / 8));
+  const int count = uniform(KI ? work_share(sg, g.groups, total, xcd + 1) : (int)((int64_t)(xcd + 1) * total / 8)) - first;
 
   struct Item {
     int e, start, i0, iv, j0, jv, klen;  // valid rows and columns of the tile; length of the reduction

@@ -10,15 +10,6 @@ namespace moe {
 
 constexpr int kW4Block = 32;
 
-// The weight at flat element i of a matrix whose rows are whole blocks.
-__device__ __forceinline__ float weight4(const uint8_t* codes, const uint8_t* scales, int64_t i) {
-  const uint32_t q = codes[i >> 1] >> (4 * (i & 1)) & 15u, s = scales[i / kW4Block];
-  const uint32_t m = q & 7u;
-  const float v = m < 2 ? 0.5f * (float)m : (float)(2 + (m & 1)) * (float)(1 << (m >> 1)) * 0.25f;
-  const float w = s == 255u ? __uint_as_float(0x7fc00000u) : ldexpf(v, (int)s - 127);
-  return q & 8u ? -w : w;
-}
-
 // Eight weights as bf16 (exact) from a dword of codes and the scale byte: the hardware's
 // conversion, which multiplies by the power of two that the float's exponent names; 255 << 23
 // gives NaN for every code, 0 stands for 2^-127.
