@@ -406,8 +406,9 @@ moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_
  * exact there) in an order fixed by the sizes, no atomics; one rounding to out_dtype.
  * n_out and k_dim multiples of 8 up to MOE_MM_MAX_DIM, ld arguments (elements from one row
  * to the next) multiples of 8 up to twice that, n_groups up to MOE_MAX_EXPERTS, rows below
- * 2^31 - 512 and n_groups (rows / 64 + 1) (max(n_out, k_dim) / 64 + 1) below 2^31; with
- * a_rows, (a_nrows + 1) rows of lda elements must fit in 4 GB - 256 B; else MOE_ERR_UNSUPPORTED.
+ * 2^31 - 512, and fewer than 2^31 pieces of 32 x 32: n_groups max(rows, min(n_out, k_dim))
+ * max(n_out, k_dim), each divided by 32, rounded down, plus 1. With a_rows, (a_nrows + 1) rows
+ * of lda elements must fit in 4 GB - 256 B. Else MOE_ERR_UNSUPPORTED.
  * No workspace. Outputs must not overlap inputs (except dw and dw_add) or each other.
  */
 #define MOE_MM_MAX_DIM (1 << 20)
@@ -449,11 +450,11 @@ moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const 
  *   op = MOE_GEMM_DOWN:    out[p] = W0[e] a[src(p)]          (codes1, scales1 unused)
  * W0 (and W1) are what codes [n_groups][n_out][k_dim / 2] and scales
  * [n_groups][n_out][k_dim / 32] stand for; a, a_rows, offsets, out, the types and the limits
- * are those of moe_grouped_mm (with n_groups (rows / 64 + 1) (max(n_out, k_dim) / 16 + 1)
- * below 2^31), k_dim a multiple of 32. Products of the weights with a are
- * exact, sums in float32. Any number of rows is taken, but every 16 rows of an expert read
- * its weights again: from about 64 rows an expert, moe_weights4_unpack and moe_grouped_mm
- * take less time. No workspace.
+ * are those of moe_grouped_mm (pieces of 16 x 16 instead of 32 x 32), k_dim a multiple of 32.
+ * Products of the weights with a are exact, sums in float32. Any number of rows is taken, but
+ * an expert's weights are read and converted again for every 16 of its rows (64 where rows >
+ * 16 n_groups): from about 32 rows an expert, moe_weights4_unpack once and moe_grouped_mm take
+ * less time. No workspace.
  */
 moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
                              const void* a, int64_t lda, const int32_t* a_rows, int64_t a_nrows,

@@ -397,6 +397,17 @@ def test_gemm4_scales_and_values_at_the_ends(dtype):
     assert (np.abs(got - ref) <= tol)[fine].all()
 
 
+def test_gemm4_of_a_nan_with_any_payload():
+    """A float32 NaN whose payload is in its last bits, of either sign, stays a NaN."""
+    codes, scales, _ = quantised(4, 1, 16, 64)
+    a = torch.ones((4, 64), device="cuda")
+    a.view(torch.int32)[1, 9] = 0x7F800001
+    a.view(torch.int32)[2, 33] = -0x7FFFFE  # 0xff800002
+    y = kept((4, 16), "f32")
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, None, codes, scales, y)
+    assert bool(torch.isnan(y[1:3]).all()) and bool(torch.isfinite(y[::3]).all())
+
+
 # ------------------------------------------------------------------- how they are used
 
 def test_two_streams_and_the_same_bits_again():

@@ -65,6 +65,13 @@ def test_common_checks(lib, op):
     for kw in (dict(G=256), dict(rows=(1 << 31) - 512), dict(n=BIG, ldo=BIG, ldy=BIG), dict(rows=1 << 30, G=255)):
         kw = {a: b for a, b in kw.items() if a in call.__code__.co_varnames}
         assert call(lib, **kw) == MOE_ERR_UNSUPPORTED, kw
+    # more pieces than 31 bits count: of rows and columns, of a weight gradient's two sides
+    wide = dict(n=1 << 20, ldo=1 << 20, ldy=1 << 20)
+    for kw in (dict(rows=1 << 17, G=255, **wide), dict(rows=1, G=255, k=1 << 20, lda=1 << 20, **wide)):
+        kw = {a: b for a, b in kw.items() if a in call.__code__.co_varnames}
+        if op == "dgrad":
+            kw["ldo"] = kw.get("k", 32)
+        assert call(lib, **kw) == MOE_ERR_UNSUPPORTED, kw
     if op != "wgrad":  # a weight gradient of no rows writes the experts' sums
         for G, off in ((4, FAKE), (1, None)):
             assert call(lib, rows=0, G=G, off=off) == MOE_OK

@@ -765,17 +765,17 @@ moe_status moe_swiglu_backward8(int64_t rows, int32_t d_ff, const int8_t* codes_
 }
 
 // Grouped products. Sizes keep a tile's byte offsets in 32 bits (256 rows of 2^20 + row
-// spacing), row numbers in 31.
+// spacing), row numbers in 31 and, whatever the offsets hold (each group all rows), the number
+// of tiles of tile x tile outputs at the least.
 static moe_status check_mm(int32_t dtype, int32_t out_dtype, int32_t groups, int32_t n_out, int32_t k_dim,
-                           int64_t rows, const int32_t* offsets, int tile = 64) {
+                           int64_t rows, const int32_t* offsets, int tile) {
   if (!row_dtype(dtype) || !row_dtype(out_dtype) || groups < 1 || n_out < 8 || n_out % 8 || k_dim < 8 || k_dim % 8 ||
       rows < 0 || (!offsets && groups != 1))
     return MOE_ERR_ARG;
   if (groups > MOE_MAX_EXPERTS || n_out > MOE_MM_MAX_DIM || k_dim > MOE_MM_MAX_DIM || rows >= (int64_t(1) << 31) - 512)
     return MOE_ERR_UNSUPPORTED;
-  // tiles (64 rows x tile columns at the least) are counted in 31 bits, whatever the offsets
-  // hold (each group all rows)
-  if (groups * (rows / 64 + 1) * (std::max(n_out, k_dim) / tile + 1) >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  const int64_t big = std::max(n_out, k_dim) / tile + 1, small = std::min(n_out, k_dim) / tile + 1;
+  if (groups * std::max(rows / tile + 1, small) * big >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
   return maybe(offsets);
 }
 // A matrix of `cols` columns whose rows are ld elements apart.
@@ -798,7 +798,7 @@ static moe_status check_mm_a(const void* a, int64_t lda, int32_t k_dim, const in
 moe_status moe_grouped_mm(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows, const void* a,
                           int64_t lda, const int32_t* a_rows, int64_t a_nrows, const int32_t* offsets, const void* w,
                           int32_t out_dtype, void* out, int64_t ldo, moe_stream stream) {
-  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets, 32));
   MOE_TRY(check_mm_a(a, lda, k_dim, a_rows, a_nrows, dtype, rows));
   MOE_TRY(need(w));
   MOE_TRY(check_mm_rows(out, ldo, n_out));
@@ -827,7 +827,7 @@ moe_status moe_grouped_mm(int32_t dtype, int32_t n_groups, int32_t n_out, int32_
 moe_status moe_grouped_mm_dgrad(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
                                 const void* dy, int64_t ldy, const int32_t* offsets, const void* w, int32_t out_dtype,
                                 void* da, int64_t lda, moe_stream stream) {
-  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets, 32));
   MOE_TRY(check_mm_rows(dy, ldy, n_out));
   MOE_TRY(need(w));
   MOE_TRY(check_mm_rows(da, lda, k_dim));
@@ -855,7 +855,7 @@ moe_status moe_grouped_mm_wgrad(int32_t dtype, int32_t n_groups, int32_t n_out, 
                                 const void* dy, int64_t ldy, const void* a, int64_t lda, const int32_t* a_rows,
                                 int64_t a_nrows, const int32_t* offsets, const float* dw_add, int32_t out_dtype,
                                 void* dw, moe_stream stream) {
-  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets));
+  MOE_TRY(check_mm(dtype, out_dtype, n_groups, n_out, k_dim, rows, offsets, 32));
   MOE_TRY(check_mm_rows(dy, ldy, n_out));
   MOE_TRY(check_mm_a(a, lda, k_dim, a_rows, a_nrows, dtype, rows));
   MOE_TRY(maybe(dw_add));

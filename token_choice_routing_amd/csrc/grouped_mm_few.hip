@@ -70,7 +70,9 @@ struct Parts<float> {
     u32x4_t a, b, c;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float x = v[j >> 1][2 * (j & 1)], y = v[j >> 1][2 * (j & 1) + 1];
+      // (a NaN whose payload is in the bits cut off would become an infinity: quiet it first)
+      const float x = __builtin_canonicalizef(v[j >> 1][2 * (j & 1)]);
+      const float y = __builtin_canonicalizef(v[j >> 1][2 * (j & 1) + 1]);
       const float x1 = cut_rest(x), y1 = cut_rest(y);
       a[j] = high_halves(x, y);
       b[j] = high_halves(x1, y1);

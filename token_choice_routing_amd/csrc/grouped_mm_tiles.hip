@@ -486,8 +486,9 @@ hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
   const int64_t slots = (int64_t)num_cus * std::max<int>(1, (int)((160 * 1024) / (lds + sizeof(Segments))));
   const unsigned blocks = (unsigned)(std::min<int64_t>(slots, mt * nt + 7) / 8 * 8);
   auto go = [&](auto kernel) {
-    (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
-                              (int)lds);
+    if (lds > 64 * 1024)
+      (void)hipFuncSetAttribute(reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)lds);
     kernel<<<blocks, 64 * WM * WN, lds, s>>>(g);
     return hipGetLastError();
   };
