@@ -16,7 +16,11 @@ struct Segments {
   int start[kMmGroups + 1];
   int len[kMmGroups + 1];
   int prefix[kMmGroups + 1];  // tiles before group e
-  int64_t cost[kMmGroups + 1];  // weight gradient: work before group e
+  // weight gradient:
+  int64_t cost[kMmGroups + 1];  // work before group e
+  int order[kMmGroups + 1];     // largest_first(): the group at a place of the order,
+  int skip[kMmGroups + 1];      // its tiles before the share,
+  int count[kMmGroups + 1];     // and those in it
 };
 
 // Group e's rows are [a, b) with a = clamp(offsets[e], 0, rows), b = clamp(offsets[e + 1], a,
@@ -108,6 +112,49 @@ __device__ __forceinline__ int work_share(const Segments& sg, int groups, int to
   const int e = max(n - 1, 0);
   const int64_t within = (at - sg.cost[e]) / (sg.len[e] + kTileCost);
   return min(sg.prefix[e] + (int)within, total);
+}
+
+// Puts the groups of the tiles [first, last) of a weight gradient in order of their rows, most
+// first, and the table's prefixes into that order (counted from 0): the workgroups of an XCD
+// then take tiles of one group after the other's as before, but those that get one tile more
+// of a group than others do so by turns among groups of like size, and the last tiles are the
+// shortest. Called by the whole workgroup; last > first.
+__device__ __forceinline__ void largest_first(Segments& sg, int groups, int first, int last) {
+  const int lo = segment_of(sg, groups, first), m = segment_of(sg, groups, last - 1) - lo + 1;
+  __syncthreads();  // every wavefront is done with the table as it was
+  if (threadIdx.x < kWave) {
+    const int lane = threadIdx.x;
+    for (int i = lane; i <= kMmGroups; i += kWave) sg.count[i] = 0;
+    for (int i = lane; i < m; i += kWave) {
+      const int e = lo + i, len = sg.len[e];
+      int rank = 0;
+      for (int f = lo; f < lo + m; ++f) {
+        const int l = sg.len[f];
+        rank += l > len || (l == len && f < e);
+      }
+      const int from = max(sg.prefix[e], first);
+      sg.order[rank] = e;
+      sg.skip[rank] = from - sg.prefix[e];
+      sg.count[rank] = min(sg.prefix[e + 1], last) - from;
+    }
+    constexpr int kPer = (kMmGroups + 1) / kWave;
+    int cnt[kPer], local = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) local += cnt[q] = sg.count[lane * kPer + q];
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < kWave; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += v;
+    }
+    int run = incl - local;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) {
+      sg.prefix[lane * kPer + q] = run;
+      run += cnt[q];
+    }
+  }
+  __syncthreads();
 }
 
 }  // namespace moe

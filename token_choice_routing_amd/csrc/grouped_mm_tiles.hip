@@ -88,14 +88,19 @@ grouped_mm_tiles_kernel(GroupedMm g) {
   const int first = uniform(KI ? work_share(sg, g.groups, total, xcd) : (int)((int64_t)xcd * total / 8));
   const int count = uniform(KI ? work_share(sg, g.groups, total, xcd + 1) : (int)((int64_t)(xcd + 1) * total / 8)) - first;
 
+  // (one tile a workgroup needs no order: it costs 1 us)
+  const bool ordered = KI && count > per;
+  if (ordered) largest_first(sg, g.groups, first, first + count);
+
   struct Item {
     int e, start, i0, iv, j0, jv, klen;  // valid rows and columns of the tile; length of the reduction
   };
   auto locate = [&](int it) __attribute__((always_inline)) {
     Item w;
-    const int t = first + it;
-    w.e = uniform(segment_of(sg, g.groups, t));
-    const int local = t - uniform(sg.prefix[w.e]);
+    const int t = ordered ? it : first + it;
+    const int at = uniform(segment_of(sg, g.groups, t));
+    w.e = ordered ? uniform(sg.order[at]) : at;
+    const int local = t - uniform(sg.prefix[at]) + (ordered ? uniform(sg.skip[at]) : 0);
     const int len = uniform(sg.len[w.e]);
     w.start = uniform(sg.start[w.e]);
     const int extent = KI ? I : len;
@@ -103,9 +108,9 @@ grouped_mm_tiles_kernel(GroupedMm g) {
     const int band = local / (kBand * nt), in = local - band * kBand * nt;
     const int high = min(kBand, mt - band * kBand);
     w.j0 = in / high * BN;
-    const int at = band * kBand + in % high, blocks = (extent + 31) / 32;
-    w.i0 = (int)((int64_t)at * blocks / mt) * 32;
-    w.iv = min((int)((int64_t)(at + 1) * blocks / mt) * 32, extent) - w.i0;
+    const int tile = band * kBand + in % high, blocks = (extent + 31) / 32;
+    w.i0 = (int)((int64_t)tile * blocks / mt) * 32;
+    w.iv = min((int)((int64_t)(tile + 1) * blocks / mt) * 32, extent) - w.i0;
     w.jv = min(BN, J - w.j0);
     w.klen = KI ? len : FORM == kMmDgrad ? g.n_out : g.k_dim;
     return w;
