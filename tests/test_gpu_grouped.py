@@ -408,6 +408,64 @@ def test_gemm4_of_a_nan_with_any_payload():
     assert bool(torch.isnan(y[1:3]).all()) and bool(torch.isfinite(y[::3]).all())
 
 
+# ------------------------------------------------------------------- past 32 bits
+
+def test_rows_past_32_bit_offsets():
+    """Segments at the end of matrices of more than 4 GB."""
+    rows, n, k = 1_100_000, 2056, 64
+    say("rows past 4 GB")
+    gen = torch.Generator(device="cuda").manual_seed(17)
+    off = torch.tensor([rows - 300, rows - 260, rows - 260, rows - 3], dtype=torch.int32, device="cuda")
+    a = torch.randn((rows, k), generator=gen, device="cuda").bfloat16()
+    dy = torch.zeros((rows, n), dtype=torch.bfloat16, device="cuda")
+    dy[rows - 300:] = torch.randn((300, n), generator=gen, device="cuda").bfloat16()
+    w = (torch.randn((3, n, k), generator=gen, device="cuda") * 0.1).bfloat16()
+    codes, scales, w4 = quantised(3, 3, n, k)
+    y, da, dw = kept((rows, n), "bf16"), kept((rows, k), "f32"), kept(w.shape, "f32")
+    tail = slice(rows - 300, rows)
+    ha, hd, hw, hf = host(a[tail]), host(dy[tail]), host(w), off.cpu().numpy() - (rows - 300)
+    tcr.moe_grouped_mm(a, off, w, y)
+    check(y[tail], *G.product(ha, hf, hw, 300), k, "bf16", "out")
+    y.fill_(KEEP)
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, off, codes, scales, y)
+    check(y[tail], *G.product(ha, hf, w4, 300), k, "bf16", "out of 4-bit weights")
+    assert bool((y[:rows - 300] == KEEP).all())
+    tcr.moe_grouped_mm_dgrad(dy, off, w, da)
+    check(da[tail], *G.data_gradient(hd, hf, hw), n, "f32", "da")
+    assert bool((da[:rows - 300] == KEEP).all())
+    tcr.moe_grouped_mm_wgrad(dy, a, off, dw)
+    check(dw, *G.weight_gradient(hd, ha, hf, 3), 257, "f32", "dw")
+
+
+def test_gathered_rows_up_to_the_limit():
+    """Row numbers at the end of the largest matrix that a_rows may name rows of."""
+    lda = 2048
+    tokens = 0xFFFFFF00 // (2 * lda) - 1
+    say(f"{tokens} tokens of {lda}")
+    a = torch.zeros((tokens, lda), dtype=torch.bfloat16, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    a[-200:] = torch.randn((200, lda), generator=gen, device="cuda").bfloat16()
+    a[:9] = torch.randn((9, lda), generator=gen, device="cuda").bfloat16()
+    rows, n = 150, 264
+    off = torch.tensor([0, 70, 140], dtype=torch.int32, device="cuda")
+    a_rows = torch.randint(tokens - 200, tokens, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    a_rows[::7] = torch.randint(0, 9, (len(a_rows[::7]),), generator=gen, device="cuda", dtype=torch.int32)
+    a_rows[3], a_rows[75] = tokens - 1, tokens + 5
+    w = (torch.randn((2, n, lda), generator=gen, device="cuda") * 0.02).bfloat16()
+    dy = torch.randn((rows, n), generator=gen, device="cuda").bfloat16()
+    ends = a[a_rows.long().clamp(0, tokens - 1)]
+    hx, hw, hd, hf = host(ends), host(w), host(dy), off.cpu().numpy()
+    y, dw = kept((rows, n), "f32"), kept(w.shape, "f32")
+    tcr.moe_grouped_mm(a, off, w, y, a_rows=a_rows)
+    check(y, *G.product(hx, hf, hw, rows), lda, "f32", "out")
+    tcr.moe_grouped_mm_wgrad(dy, a, off, dw, a_rows=a_rows)
+    check(dw, *G.weight_gradient(hd, hx, hf, 2), 70, "f32", "dw")
+    with pytest.raises(tcr.MoeError) as e:
+        more = torch.empty((tokens + 1, lda), dtype=torch.bfloat16, device="cuda")
+        tcr.moe_grouped_mm(more, off, w, y, a_rows=a_rows)
+    assert e.value.status == tcr.MOE_ERR_UNSUPPORTED
+
+
 # ------------------------------------------------------------------- how they are used
 
 def test_two_streams_and_the_same_bits_again():
