@@ -141,6 +141,9 @@ __device__ __forceinline__ f32x4_t mfma_few(bf16x8_t w, bf16x8_t a, f32x4_t c) {
 template <typename T, bool W4, bool SWIGLU, int KS, int MT>
 __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
   constexpr int kRows = 16 * MT;
+  // of more than 16 rows two sixteens in turn (64 experts of 32 rows: 96 -> 69 us in bf16; float32
+  // ones would take too many registers: 131 -> 157)
+  constexpr int NA = MT == 1 || sizeof(T) == 4 ? 1 : 2;
   constexpr int NP = W4 ? Parts<T>::N : 1;
   constexpr int OC = SWIGLU ? 16 : 32, WC = OC * (4 / KS);  // output columns of an item, of the workgroup
   __shared__ Segments sg;
@@ -169,17 +172,17 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
       auto col = [&](int c, int i) { return c * kChunk + (W4 ? 32 * j + 8 * i : 32 * i + 8 * j); };
       struct Set {  // a chunk in registers; two in turn
         Weights<T, W4> w[2];
-        Parts<T> a[4];
+        Parts<T> a[NA][4];
       };
       auto load_rows = [&](Set& s, int m, int c) __attribute__((always_inline)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s.a[i].load(arow[m] + (col(c, i) < K ? col(c, i) : 0));
+        for (int i = 0; i < 4; ++i) s.a[m % NA][i].load(arow[m] + (col(c, i) < K ? col(c, i) : 0));
       };
       auto load = [&](Set& s, int c) __attribute__((always_inline)) {
         if (c >= c1) return;
 #pragma unroll
         for (int b = 0; b < 2; ++b) s.w[b].load(base[b], c, j, K);
-        if (MT == 1) load_rows(s, 0, c);
+        load_rows(s, 0, c);
       };
       Set s0, s1;
       auto multiply = [&](Set& s, int c) __attribute__((always_inline)) {
@@ -192,13 +195,14 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
           if (MT > 1 && 16 * m >= rows) break;
-          if (MT > 1) load_rows(s, m, c);
+          if (NA == 1 && m > 0) load_rows(s, m, c);
+          if (NA == 2 && m + 1 < MT && 16 * (m + 1) < rows) load_rows(s, m + 1, c);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            s.a[i].keep(col(c, i) < K);
+            s.a[m % NA][i].keep(col(c, i) < K);
             bf16x8_t p[NP];
-            if constexpr (W4) s.a[i].split(p);
-            else p[0] = __builtin_bit_cast(bf16x8_t, s.a[i].v);
+            if constexpr (W4) s.a[m % NA][i].split(p);
+            else p[0] = __builtin_bit_cast(bf16x8_t, s.a[m % NA][i].v);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
         if (g.a_rows) row = min<int64_t>(max<int64_t>(g.a_rows[row], 0), g.a_nrows - 1);
         arow[m] = static_cast<const T*>(g.a) + row * g.lda;
       }
-      if (MT == 1 && c0 < c1) load_rows(s0, 0, c0);
+      if (c0 < c1) load_rows(s0, 0, c0);
       load(s1, c0 + 1);
       for (int c = c0; c < c1; c += 2) {
         multiply(s0, c);
@@ -280,8 +284,8 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
 // Rules (us at 64 experts, n 2048, k 1536, bf16): a wavefront takes the whole reduction where
 // there are items for most of them (64 rows: 33 against 40 with a quarter each; 2 rows of two
 // experts, n 1536, k 2048: 13 against 8); 64 rows an item where an expert has more than 16
-// (64 rows: 41 against 37 with 16; 1024 rows: 47 and 46; with 32 rows an expert 69 for 64, as
-// 16 read and convert every weight twice).
+// (64 rows: 41 against 37 with 16; 1024 rows: 47 and 46; with 32 rows an expert 69, where 16
+// would read and convert every weight twice).
 hipError_t launch_grouped_mm_few(const GroupedMm& g, int num_cus, hipStream_t s) {
   const bool swiglu = g.form == kMm4Swiglu, tall = g.rows > 16 * (int64_t)g.groups;
   const int oc = swiglu ? 16 : 32;
