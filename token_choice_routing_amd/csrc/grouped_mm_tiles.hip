@@ -74,7 +74,8 @@ __device__ __forceinline__ void deal(int n, F&& f) {
   else deal<N - 1>(n, f);
 }
 
-template <typename T, int FORM, int BM, int BN, int WM, int WN, int S>
+// ROWS: a weight gradient whose a is read through a_rows (then rows > 0).
+template <typename T, int FORM, bool ROWS, int BM, int BN, int WM, int WN, int S>
 __global__ void __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2, 2)))
 grouped_mm_tiles_kernel(GroupedMm g) {
   constexpr int ES = sizeof(T), EC = 16 / ES, kBK = 64 / ES;  // bytes an element; elements of 16 bytes, of a stage's row
@@ -159,7 +160,7 @@ grouped_mm_tiles_kernel(GroupedMm g) {
     for (int p = 0; p < PJ; ++p)
 #pragma unroll
       for (int q = 0; q < KPP; ++q) {
-        const int k = min(lkt * kBK + (wave + NW * p) * KPP + q, lklen - 1);
+        const int k = min(lkt * kBK + (wave + NW * p) * KPP + q, max(lklen - 1, 0));
         idx[p][q] = a_rows[(uint32_t)uniform(lstart + k)];
       }
   };
@@ -204,24 +205,24 @@ grouped_mm_tiles_kernel(GroupedMm g) {
         }
       }
       const T* jbase;
-      if (FORM == kMmWgrad) jbase = static_cast<const T*>(g.a) + (g.a_rows ? 0 : (int64_t)w.start * g.lda) + w.j0;
+      if (FORM == kMmWgrad) jbase = static_cast<const T*>(g.a) + (ROWS ? 0 : (int64_t)w.start * g.lda) + w.j0;
       else if (FORM == kMmDgrad) jbase = static_cast<const T*>(g.w) + (int64_t)w.e * g.n_out * g.k_dim + w.j0;
       else jbase = static_cast<const T*>(g.w) + ((int64_t)w.e * g.n_out + w.j0) * g.k_dim;
       jsrc = uniform_ptr(jbase);
       const int64_t jld = FORM == kMmWgrad ? g.lda : g.k_dim;
-      jstep = KJ ? (FORM == kMmWgrad && g.a_rows ? 0 : kBK * jld) : kBK;
+      jstep = KJ ? (ROWS ? 0 : kBK * jld) : kBK;
 #pragma unroll
       for (int p = 0; p < PJ; ++p) {
         if constexpr (KJ) {
           const int kr = krow(wave + NW * p, BN), c = kcol(kr, BN);
-          const bool rowless = FORM == kMmWgrad && g.a_rows;  // the row is added at each tile
-          joff[p] = c < w.jv ? (uint32_t)((rowless ? 0 : kr * jld) + c) * ES : kPast;
+          // (of gathered rows: the row is added at each tile)
+          joff[p] = c < w.jv ? (uint32_t)((ROWS ? 0 : kr * jld) + c) * ES : kPast;
         } else {
           const int r = 16 * (wave + NW * p) + (lane >> 2);
           joff[p] = r < w.jv ? (uint32_t)(r * jld + lc * EC) * ES : kPast;
         }
       }
-      if (FORM == kMmWgrad && g.a_rows) fetch_rows();
+      if constexpr (ROWS) fetch_rows();
       fetch_next();
       return;
     }
@@ -243,7 +244,7 @@ grouped_mm_tiles_kernel(GroupedMm g) {
       const int piece = wave + NW * p;
       const int k = k0 + (KJ ? krow(piece, BN) : lc * EC);
       uint32_t off = joff[p];
-      if (FORM == kMmWgrad && g.a_rows) {
+      if constexpr (ROWS) {
         int row = idx[p][0];
 #pragma unroll
         for (int q = 1; q < KPP; ++q) row = lane / (BN * ES / 16) >= q ? idx[p][q] : row;
@@ -260,9 +261,9 @@ grouped_mm_tiles_kernel(GroupedMm g) {
   // waited for first: scalar loads return in no order, so an LDS wait behind them would be one
   // for everything.
   auto before_issue = [&]() __attribute__((always_inline)) {
-    if (FORM == kMmWgrad && g.a_rows) {
+    if constexpr (ROWS) {
       __builtin_amdgcn_s_waitcnt((63 & 15) | ((63 >> 4) << 14) | (7 << 4));  // lgkmcnt(0)
-      if (lkt < lnk) fetch_rows();
+      fetch_rows();  // (past an item's end: some row of it; the next item's are read when it is opened)
     }
   };
 
@@ -508,9 +509,11 @@ hipError_t launch_tiles(const GroupedMm& g, int num_cus, hipStream_t s) {
     return hipGetLastError();
   };
   switch (g.form) {
-    case kMm: return go(grouped_mm_tiles_kernel<T, kMm, BM, BN, WM, WN, S>);
-    case kMmDgrad: return go(grouped_mm_tiles_kernel<T, kMmDgrad, BM, BN, WM, WN, S>);
-    case kMmWgrad: return go(grouped_mm_tiles_kernel<T, kMmWgrad, BM, BN, WM, WN, S>);
+    case kMm: return go(grouped_mm_tiles_kernel<T, kMm, false, BM, BN, WM, WN, S>);
+    case kMmDgrad: return go(grouped_mm_tiles_kernel<T, kMmDgrad, false, BM, BN, WM, WN, S>);
+    case kMmWgrad:
+      return g.a_rows && g.rows ? go(grouped_mm_tiles_kernel<T, kMmWgrad, true, BM, BN, WM, WN, S>)
+                                : go(grouped_mm_tiles_kernel<T, kMmWgrad, false, BM, BN, WM, WN, S>);
   }
   return hipErrorInvalidValue;
 }
