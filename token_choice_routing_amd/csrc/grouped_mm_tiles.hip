@@ -406,7 +406,7 @@ grouped_mm_tiles_kernel(GroupedMm g) {
       if constexpr (KI) {
         const bool whole = (g.k_dim * sizeof(type)) % 128 == 0 && reinterpret_cast<uintptr_t>(g.out) % 128 == 0;
         if (g.add) store(type, std::true_type{}, std::false_type{}, w, acc, stage);
-        else if (whole) store(type, std::false_type{}, std::true_type{}, w, acc, stage);
+        else if (sizeof(type) == 4 && whole) store(type, std::false_type{}, std::true_type{}, w, acc, stage);
         else store(type, std::false_type{}, std::false_type{}, w, acc, stage);
       } else {
         store(type, std::false_type{}, std::false_type{}, w, acc, stage);
@@ -433,7 +433,7 @@ grouped_mm_tiles_kernel(GroupedMm g) {
   };
 
   if (slot >= count) return;
-#pragma unroll
+#pragma unroll 1  // (opening an item is long code, which should stay in the instruction cache)
   for (int s = 0; s < S; ++s) {
     before_issue();
     issue(s);
