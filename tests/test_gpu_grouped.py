@@ -81,6 +81,7 @@ SHAPES = [
     ([300, 0, 1, 257, 513], 328, 264),
     ([700], 512, 256),
     ([3] * 60, 136, 1016),
+    ([0, 1, 2, 0, 70] * 51, 24, 40),  # MOE_MAX_EXPERTS
 ]
 
 
@@ -341,6 +342,7 @@ SHAPES4 = [
     ([3] * 60, 136, 1024),
     ([100, 0, 257], 40, 96),
     ([2, 0, 9], 16, 2080),
+    ([0, 1, 2, 0, 70] * 51, 24, 64),  # MOE_MAX_EXPERTS
 ]
 
 
