@@ -435,7 +435,8 @@ moe_status moe_grouped_mm_wgrad(int32_t dtype, int32_t n_groups, int32_t n_out, 
  * This is MXFP4 (OCP microscaling: blocks of 32, e2m1 elements, a power of two per block),
  * and scale bytes of other origin are taken as it defines them (0 is 2^-127). A block with
  * a NaN or an infinity has scale byte 255 and codes 0 and stands for NaN.
- * |w - value| <= amax / 4 at the top of a block (between 6 and 8 steps), amax / 8 elsewhere.
+ * |w - value| <= 2^e / 4 up to 2 steps of 2^e, 2^e / 2 up to 4, 2^e up to 6, and below 2^(e+1)
+ * beyond (amax lies in [4, 8) steps, so always below amax / 4; blocks below 2^-124 apart).
  * rows >= 0 (0 is a no-op), rows * cols below 2^40. No workspace.
  */
 moe_status moe_weights4_pack(int64_t rows, int32_t cols, int32_t dtype, const void* w, uint8_t* codes, uint8_t* scales,

@@ -64,6 +64,21 @@ def test_pack4_takes_the_nearest_value():
     np.testing.assert_array_equal(got >> 4, code[:, 1::2])
 
 
+def test_pack4_error_by_size():
+    """|w - value| by the size of w in steps: a quarter of a step up to 2, half up to 4, one up to
+    6, below two beyond; below a quarter of the block's largest in all."""
+    rng = np.random.default_rng(8)
+    w = rng.uniform(-1, 1, (500, 64)) * 2.0 ** rng.uniform(-8, 8, (500, 1))
+    _, scale, v = G.pack4(w)
+    step = np.repeat(2.0 ** (scale.astype(float) - 127), 32, 1)
+    m, err = np.abs(w) / step, np.abs(w - v) / step
+    for lo, hi, most in ((0, 2, 0.25), (2, 4, 0.5), (4, 6, 1.0), (6, 8, 2.0)):
+        here = (m >= lo) & (m <= hi)
+        assert here.any() and (err[here] <= most).all()
+    amax = np.repeat(np.abs(w.reshape(500, 2, 32)).max(-1), 32, 1)
+    assert (np.abs(w - v) < amax / 4).all()
+
+
 def test_pack4_ties_and_ends():
     row = np.zeros((1, 32))
     row[0, :9] = [4.0, 0.25, -0.75, 1.25, 1.75, 2.5, -3.5, 5.0, 6.5]

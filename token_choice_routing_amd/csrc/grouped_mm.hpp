@@ -121,7 +121,8 @@ __device__ __forceinline__ int work_share(const Segments& sg, int groups, int to
 // first, and the table's prefixes into that order (counted from 0): the workgroups of an XCD
 // then take tiles of one group after the other's as before, but those that get one tile more
 // of a group than others do so by turns among groups of like size, and the last tiles are the
-// shortest (experts as uneven as exp(0.5 N(0, 1)) in popularity: 356 us without, 332 so). Called by the whole workgroup; last > first.
+// shortest (32768 rows of 64 experts as uneven as routing of skewed popularity makes them: 356 us
+// without, 332 so). Called by the whole workgroup; last > first.
 __device__ __forceinline__ void largest_first(Segments& sg, int groups, int first, int last) {
   const int lo = segment_of(sg, groups, first), m = segment_of(sg, groups, last - 1) - lo + 1;
   __syncthreads();  // every wavefront is done with the table as it was
