@@ -537,6 +537,34 @@ def test_captured_in_a_graph():
             assert bool((r == g).all()), i
 
 
+def test_many_tiles_captured_in_a_graph():
+    n, k = 1032, 1040
+    rows, off, a_rows, a, dy, w = make(31, MANY, n, k, "bf16", T=900)
+
+    def outputs():
+        return kept((rows, n), "bf16"), kept((rows, k), "bf16"), kept(w.shape, "f32")
+
+    def run(o):
+        tcr.moe_grouped_mm(a, off, w, o[0], a_rows=a_rows)
+        tcr.moe_grouped_mm_dgrad(dy, off, w, o[1])
+        tcr.moe_grouped_mm_wgrad(dy, a, off, o[2], a_rows=a_rows)
+
+    ref, got = outputs(), outputs()
+    run(ref)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(got)
+    for _ in range(3):
+        for t in got:
+            t.fill_(KEEP)
+        graph.replay()
+        run(ref)
+        torch.cuda.synchronize()
+        for r, g in zip(ref, got):
+            assert bool((r == g).all())
+
+
 def _dispatch(T, d, N, K, seed):
     """Routing of T random tokens as the layer's own entry points leave it."""
     gen = torch.Generator(device="cuda").manual_seed(seed)
