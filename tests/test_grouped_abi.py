@@ -123,6 +123,22 @@ def test_weights4_checks(lib):
         assert call(rows=0) == MOE_OK
 
 
+def test_weights4_sizes_whose_product_passes_64_bits(lib):
+    """rows * cols of 2^40 and more are refused, also where the product as 64 bits is small or
+    negative, and the largest size below that is not."""
+    most = 2 ** 31 - 32
+    sizes = [((1 << 40) // 64, 64), ((1 << 40) // most + 1, most), (1 << 39, 1 << 26), (1 << 38, 1 << 26),
+             (1 << 39, 1 << 24), ((1 << 40) - 1, most), ((1 << 63) - 1, 32), ((1 << 63) - 1, most)]
+    for rows, cols in sizes:
+        assert rows * cols >= 1 << 40
+        assert lib.moe_weights4_pack(rows, cols, MOE_F32, FAKE, FAKE, FAKE, None) == MOE_ERR_UNSUPPORTED, (rows, cols)
+        assert lib.moe_weights4_unpack(rows, cols, MOE_F32, FAKE, FAKE, FAKE, None) == MOE_ERR_UNSUPPORTED, (rows, cols)
+    # (a misaligned pointer, which is looked at after the sizes)
+    for rows, cols in (((1 << 40) // 64 - 1, 64), ((1 << 40) // most, most), (1 << 34, 32)):
+        assert rows * cols < 1 << 40
+        assert lib.moe_weights4_pack(rows, cols, MOE_F32, MIS, FAKE, FAKE, None) == MOE_ERR_ALIGN, (rows, cols)
+
+
 def test_binding_refuses():
     """Tensors on the host, of another type or shape, or missing."""
     z = torch.zeros

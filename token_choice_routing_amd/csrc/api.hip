@@ -926,7 +926,7 @@ moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_
 
 static moe_status check_weights4(int64_t rows, int32_t cols, int32_t dtype) {
   if (rows < 0 || cols < 32 || cols % 32 || !row_dtype(dtype)) return MOE_ERR_ARG;
-  if (rows >= (int64_t(1) << 40) || rows * cols >= (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+  if (rows > ((int64_t(1) << 40) - 1) / cols) return MOE_ERR_UNSUPPORTED;  // (the product may pass 64 bits)
   return MOE_OK;
 }
 
