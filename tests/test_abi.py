@@ -283,3 +283,21 @@ def test_noalloc_entry_checks(lib):
     assert tcr.workspace_bytes(big, MOE_WS_LAYER) > tcr.MOE_NOALLOC_MAX_WS_BYTES
     p = tcr.LayerParams(FAKE, FAKE, 0.0, None, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE)
     assert lib.moe_layer_forward_noalloc(ctypes.byref(big), ctypes.byref(p), FAKE, None, None) == MOE_ERR_UNSUPPORTED
+
+
+def test_sizes_whose_products_pass_64_bits(lib):
+    """T * K of 2^31 and more, and 2^40 and more elements of rows, are refused also where
+    their product as 64 bits is small or negative; the largest sizes below are not."""
+    for T, K in ((1 << 62, 4), (1 << 61, 8), ((1 << 63) - 1, 2), ((1 << 31) // 2, 2), ((1 << 31) - 1, 2)):
+        d = make_dims(T=T, d_model=64, n_experts=8, n_null=8, top_k=K, d_ff=64)
+        assert lib.moe_combine(ctypes.byref(d), FAKE, FAKE, FAKE, None, None, FAKE, None) == MOE_ERR_UNSUPPORTED, (T, K)
+        assert tcr.workspace_bytes(d) == 0
+    d = make_dims(T=(1 << 31) // 3, d_model=64, n_experts=8, n_null=8, top_k=3, d_ff=64)
+    assert lib.moe_combine(ctypes.byref(d), MIS, FAKE, FAKE, None, None, FAKE, None) == MOE_ERR_ALIGN
+    d = make_dims(T=16, d_model=64, n_experts=8, n_null=8, top_k=2, d_ff=64, dtype=MOE_F32)
+    big = (1 << 64) - 1
+    for rows in (1 << 34, 1 << 58, 1 << 60, (1 << 63) - 1):
+        assert lib.moe_expert_ffn(ctypes.byref(d), 2, 64, rows, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, big,
+                                  None) == MOE_ERR_UNSUPPORTED, rows
+    assert lib.moe_expert_ffn(ctypes.byref(d), 2, 64, (1 << 34) - 1, MIS, FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, big,
+                              None) == MOE_ERR_ALIGN

@@ -34,7 +34,7 @@ moe_status check_dims(const moe_dims* d) {
   if (d->n_experts > MOE_MAX_EXPERTS || d->top_k > MOE_MAX_TOPK ||
       (int64_t)d->n_experts + d->n_null > MOE_MAX_POOL)
     return MOE_ERR_UNSUPPORTED;
-  if (d->T * (int64_t)d->top_k >= (int64_t(1) << 31)) return MOE_ERR_UNSUPPORTED;
+  if (d->T > ((int64_t(1) << 31) - 1) / d->top_k) return MOE_ERR_UNSUPPORTED;  // (the product may pass 64 bits)
   return MOE_OK;
 }
 
@@ -499,7 +499,7 @@ moe_status moe_expert_ffn(const moe_dims* d, int32_t n_groups, int32_t d_ff, int
   if (n_groups < 1 || n_groups > MOE_MAX_EXPERTS + 1 || d_ff < 8 || d_ff % 8 || rows < 0)
     return MOE_ERR_ARG;
   if (!offsets && n_groups != 1) return MOE_ERR_ARG;
-  if (rows * (int64_t)std::max(d->d_model, d_ff) >= (int64_t(1) << 40)) return MOE_ERR_UNSUPPORTED;
+  if (rows > ((int64_t(1) << 40) - 1) / std::max(d->d_model, d_ff)) return MOE_ERR_UNSUPPORTED;
   if (d->dtype == MOE_BF16 && !fits_4g(d_ff, d->d_model)) return MOE_ERR_UNSUPPORTED;
   MOE_TRY(need(a));
   MOE_TRY(maybe(offsets));
