@@ -410,6 +410,101 @@ def test_gemm4_of_a_nan_with_any_payload():
     assert bool(torch.isnan(y[1:3]).all()) and bool(torch.isfinite(y[::3]).all())
 
 
+# Kernel forms that the sizes above leave out, with 256 CUs.
+# At most 16 rows an expert and at least 1024 items: a wavefront takes the whole reduction (of 16
+# rows). 968 columns end inside a panel of 128 (64 for gate/up): of its four wavefronts one has
+# columns in part and one or more have none.
+FEW_WHOLE = [0, 3, 9, 1, 5, 0, 2, 8, 4, 7, 16, 0] * 5
+# More than 16 rows an expert: 64 rows an item, a wavefront with the whole reduction.
+TALL_WHOLE = [17, 70, 0, 33, 64, 65, 1, 48, 20, 5, 16, 130]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("n,k", [(968, 544), (1000, 72)])
+def test_few_rows_with_the_whole_reduction(n, k, gather, out, dtype):
+    say(f"few rows, whole reduction n {n} k {k} {dtype} -> {out} gather {gather}")
+    rows, off, a_rows, a, _, w = make(51, FEW_WHOLE, n, k, dtype, T=40 if gather else None, first=1)
+    assert rows <= 16 * len(FEW_WHOLE) and (rows // 16 + len(FEW_WHOLE)) * (n // 32) >= 1024
+    y = kept((rows, n + 8), out)
+    tcr.moe_grouped_mm(a, off, w, y[:, :n], a_rows=a_rows)
+    ha, hf, hw, hr = arrays(a, off, w, a_rows)
+    check(y[:, :n], *G.product(ha, hf, hw, rows, hr), k, out, "out")
+    assert bool((y[:, n:] == KEEP).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("out", TYPES)
+@pytest.mark.parametrize("counts,n,k", [(FEW_WHOLE, 968, 544), (TALL_WHOLE, 2056, 160)])
+def test_gemm4_with_the_whole_reduction(counts, n, k, out, dtype):
+    """A wavefront with the whole reduction of 16 or of 64 rows, plain and gate/up."""
+    c0, s0, w0 = quantised(61, len(counts), n, k)
+    c1, s1, w1 = quantised(62, len(counts), n, k)
+    for gather in (False, True):
+        say(f"gemm4, whole reduction {len(counts)} experts n {n} k {k} {dtype} -> {out} gather {gather}")
+        rows, off, a_rows, a, _, _ = make(52, counts, n, k, dtype, T=70 if gather else None, first=1)
+        per = 64 if rows > 16 * len(counts) else 16
+        assert per == (16 if counts is FEW_WHOLE else 64) and (rows // per + len(counts)) * (n // 32) >= 1024
+        ha, hf, hr = arrays(a, off, a_rows)
+        (g, mg), (u, mu) = G.product(ha, hf, w0, rows, hr), G.product(ha, hf, w1, rows, hr)
+        y = kept((rows, n), out)
+        tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, off, c0, s0, y, a_rows=a_rows)
+        check(y, g, mg, 3 * k, out, "down")
+        y = kept((rows, n + 8), out)
+        tcr.moe_grouped_gemm4(tcr.MOE_GEMM_GATE_UP, a, off, c0, s0, y[:, :n], c1, s1, a_rows=a_rows)
+        check_swiglu(y[:, :n], g, mg, u, mu, 3 * k, out, "gate/up")
+        assert bool((y[:, n:] == KEEP).all())
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("n,k,out,added", [(264, 520, "f32", False), (264, 520, "f32", True), (520, 136, "bf16", True),
+                                           (136, 544, "f16", False)])
+def test_many_tiles_of_float32(n, k, out, added, gather):
+    """128 x 128 float32 tiles with every number of 32-row blocks, several row tiles and column
+    tiles an expert, and many stages of the reduction in all three forms."""
+    say(f"many tiles n {n} k {k} f32 -> {out} added {added} gather {gather}")
+    rows, off, a_rows, a, dy, w = make(32, MANY, n, k, "f32", T=900 if gather else None)
+    groups = len(MANY)
+    assert (rows // 128 + groups) * (n // 128) >= 128 and groups * (n // 128) * (k // 128) >= 256
+    dw, add = kept(w.shape, out), None
+    if added:
+        add = torch.randn(w.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    y, da = kept((rows, n), out), kept((rows, k), out)
+    ha, hf, hw, hr, hd, hadd = arrays(a, off, w, a_rows, dy, add)
+    tcr.moe_grouped_mm(a, off, w, y, a_rows=a_rows)
+    check(y, *G.product(ha, hf, hw, rows, hr), k, out, "out")
+    tcr.moe_grouped_mm_dgrad(dy, off, w, da)
+    check(da, *G.data_gradient(hd, hf, hw), n, out, "da")
+    ref, mag = G.weight_gradient(hd, ha, hf, groups, hadd, hr)
+    tcr.moe_grouped_mm_wgrad(dy, a, off, dw, a_rows=a_rows, dw_add=add)
+    check(dw, ref, mag, max(MANY) + 1, out, "dw")
+    if added:
+        tcr.moe_grouped_mm_wgrad(dy, a, off, add, a_rows=a_rows, dw_add=add)
+        check(add, ref, mag, max(MANY) + 1, "f32", "dw in place")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("gather", [False, True])
+def test_large_weight_gradient_in_float32(gather, dtype):
+    """256 x 256 tiles whose rows of the gradient are whole 128-byte lines, which are stored past
+    the caches; and the same ones added to an earlier gradient, also in place."""
+    n, k = 520, 544
+    say(f"large weight gradient n {n} k {k} {dtype} -> f32 gather {gather}")
+    rows, off, a_rows, a, dy, w = make(33, MANY, n, k, dtype, T=900 if gather else None)
+    add = torch.randn(w.shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    ha, hf, hr, hd, hadd = arrays(a, off, a_rows, dy, add)
+    dw = kept(w.shape, "f32")
+    tcr.moe_grouped_mm_wgrad(dy, a, off, dw, a_rows=a_rows)
+    check(dw, *G.weight_gradient(hd, ha, hf, len(MANY), None, hr), max(MANY), "f32", "dw")
+    ref, mag = G.weight_gradient(hd, ha, hf, len(MANY), hadd, hr)
+    dw.fill_(KEEP)
+    tcr.moe_grouped_mm_wgrad(dy, a, off, dw, a_rows=a_rows, dw_add=add)
+    check(dw, ref, mag, max(MANY) + 1, "f32", "dw added")
+    tcr.moe_grouped_mm_wgrad(dy, a, off, add, a_rows=a_rows, dw_add=add)
+    check(add, ref, mag, max(MANY) + 1, "f32", "dw in place")
+
+
 # ------------------------------------------------------------------- past 32 bits
 
 def test_rows_past_32_bit_offsets():
