@@ -441,7 +441,8 @@ moe_status moe_grouped_mm_wgrad(int32_t dtype, int32_t n_groups, int32_t n_out, 
  */
 moe_status moe_weights4_pack(int64_t rows, int32_t cols, int32_t dtype, const void* w, uint8_t* codes, uint8_t* scales,
                              moe_stream stream);
-/* The values 4-bit weights stand for, rounded to dtype (exact in MOE_F32 and MOE_BF16). */
+/* The values 4-bit weights stand for, rounded to dtype (exact in MOE_F32 and MOE_BF16 below
+ * 2^128; what scale bytes 253 and 254 name beyond that becomes infinite). */
 moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const uint8_t* codes, const uint8_t* scales,
                                void* out, moe_stream stream);
 
@@ -452,7 +453,8 @@ moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const 
  * W0 (and W1) are what codes [n_groups][n_out][k_dim / 2] and scales
  * [n_groups][n_out][k_dim / 32] stand for; a, a_rows, offsets, out, the types and the limits
  * are those of moe_grouped_mm (pieces of 16 x 16 instead of 32 x 32), k_dim a multiple of 32.
- * Products of the weights with a are exact, sums in float32. Any number of rows is taken, but
+ * Products of the weights with a are exact (of weights of 2^128 and more too: an output is
+ * infinite only if its sum or a part of it is too large), sums in float32. Any number of rows is taken, but
  * an expert's weights are read and converted again for every 16 of its rows (64 where rows >
  * 16 n_groups): from about 32 rows an expert, moe_weights4_unpack once and moe_grouped_mm take
  * less time. No workspace.

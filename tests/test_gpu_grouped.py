@@ -399,6 +399,95 @@ def test_gemm4_scales_and_values_at_the_ends(dtype):
     assert (np.abs(got - ref) <= tol)[fine].all()
 
 
+# groups, rows of each and the wavefronts that share a reduction (n 256): four or one, of 16 or
+# of 64 rows
+SPLITS = [(1, 5), (1, 40), (128, 2), (120, 17)]
+EXPONENTS = {"bf16": (0, -130, -100, -60, 60, 100, 118), "f16": (0, -14, -20, 4, 9),
+             "f32": (0, -100, -60, 60, 100, 118)}
+
+
+def check_extreme(got, ref, mag, K, top, what):
+    """Products and sums as in check(), each operation further off by half the smallest float32
+    (eight of them in a weight row with a byte above 252, whose sums are held divided by 8: `top`).
+    Where the terms' magnitudes add up to 2^128, a partial sum may be infinite; below, none is."""
+    got = host(got)
+    tol = (3 * K + 1) * 2.0 ** -23 * mag + rounding(ref, "f32") + 3 * K * 2.0 ** -149 * np.where(top, 8, 1)
+    finite = mag * (1 + 3 * K * 2.0 ** -23) < 2.0 ** 128
+    nan = np.isnan(ref)
+    assert np.isnan(got[nan]).all(), what
+    with np.errstate(invalid="ignore"):
+        off = np.abs(got - ref) / tol
+    worst = float(off[finite & ~nan].max())
+    say(f"  {what}: worst {worst:.3f} of the tolerance, {int((~finite).sum())} of {finite.size} may pass 2^128")
+    assert worst <= 1.0, (what, worst)
+    return finite
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("groups,each", SPLITS)
+def test_gemm4_of_every_scale_byte(groups, each, dtype):
+    """Weight row r has scale byte r, alone or next to other bytes, with rows of all sizes: no
+    product or sum that a float32 can hold is lost."""
+    n, k = 256, 160
+    say(f"every scale byte, {groups} groups of {each} rows, {dtype}")
+    rows = groups * each
+    gen = torch.Generator(device="cuda").manual_seed(71)
+    off = torch.arange(0, rows + 1, each, dtype=torch.int32, device="cuda")
+    e = torch.tensor([EXPONENTS[dtype][i % len(EXPONENTS[dtype])] for i in range(rows)], device="cuda")
+    a = torch.randn((rows, k), generator=gen, device="cuda", dtype=torch.float64) * torch.exp2(e.double())[:, None]
+    a[:, 40:44] = 0.0
+    a = a.to(TYPES[dtype])
+    codes, _, _ = quantised(72, groups, n, k)
+    scales = torch.arange(256, dtype=torch.uint8, device="cuda")[None, :, None].expand(groups, n, 5).contiguous()
+    other = torch.randint(0, 255, scales.shape, generator=gen, device="cuda", dtype=torch.uint8)
+    for name, mixed in (("one byte a row", scales), ("first block", torch.cat((scales[..., :1], other[..., 1:]), 2)),
+                        ("last block", torch.cat((other[..., :4] // 2, scales[..., 4:]), 2))):
+        h, hs = codes.cpu().numpy(), mixed.cpu().numpy()
+        w = G.values4(np.stack([h & 15, h >> 4], -1).reshape(groups, n, k), hs)
+        y = kept((rows, n), "f32")
+        tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, off, codes, mixed, y)
+        ref, mag = G.product(host(a), off.cpu().numpy(), w, rows)
+        top = np.repeat(((hs == 253) | (hs == 254)).any(2), each, 0)
+        assert check_extreme(y, ref, mag, k, top, name)[top].any()
+    # up weights alone that reach 2^128: h = silu(g) u with u as above
+    g_codes, g_scales, gw = quantised(73, groups, n, k, 80, 85)
+    small = torch.where(a.abs() < 2, a, 0.0).to(a.dtype) if dtype != "f16" else (a.float() * 2.0 ** -12).half()
+    ref_u, mag = G.product(host(small), off.cpu().numpy(), w, rows)
+    ref_g, mag_g = G.product(host(small), off.cpu().numpy(), gw, rows)
+    y = kept((rows, n), "f32")
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_GATE_UP, small, off, g_codes, g_scales, y, codes, mixed)
+    # |silu(g)| <= |g|, and sigmoid(g) is 1/2 to within 2^-20 here
+    assert np.abs(ref_g).max() < 2.0 ** -20
+    fine = (mag * (1 + 3 * k * 2.0 ** -23) < 2.0 ** 128) & (mag_g * mag < 2.0 ** 126) & ~np.isnan(ref_u)
+    tol = (8 * k + 40) * 2.0 ** -23 * mag_g * mag + 2.0 ** -20 * np.abs(ref_g * ref_u)
+    tol += np.abs(ref_g) * 3 * k * 2.0 ** -146 + (np.abs(ref_u) + 1) * 3 * k * 2.0 ** -149
+    err = np.abs(host(y) - ref_g * ref_u / 2)
+    assert fine[:, 253:255].any() and (err <= tol)[fine].all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_gemm4_of_values_past_the_largest_float(dtype):
+    """Weights of 2^128 and more: exact where the product is not too large, infinite where it
+    is, 0 times a zero, NaN only with an infinity times a zero code or a NaN."""
+    codes = torch.zeros((1, 16, 32), dtype=torch.uint8, device="cuda")
+    codes[0, :8, :] = 0x77    # 6
+    codes[0, 8:12, :] = 0xFF  # -6
+    codes[0, 12:, 0] = 0x64   # 2 and 4, then zeros
+    scales = torch.full((1, 16, 2), 254, dtype=torch.uint8, device="cuda")
+    scales[0, 4:8] = 253
+    a = torch.zeros((5, 64), device="cuda")
+    a[1], a[2, 0], a[3, 1], a[4, 0] = 1.0, 2.0 ** -14, 1.0, float("inf")
+    y = kept((5, 16), "f32")
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a.to(TYPES[dtype]), None, codes, scales, y)
+    got, inf = host(y), np.inf
+    assert (got[0] == 0).all()
+    assert (got[1] == [inf] * 8 + [-inf] * 4 + [inf] * 4).all()
+    top = 6 * 2.0 ** 113
+    assert (got[2] == [top] * 4 + [top / 2] * 4 + [-top] * 4 + [2.0 ** 114] * 4).all()
+    assert (got[3] == [inf] * 8 + [-inf] * 4 + [inf] * 4).all()
+    assert (got[4] == [inf] * 8 + [-inf] * 4 + [inf] * 4).all()
+
+
 def test_gemm4_of_a_nan_with_any_payload():
     """A float32 NaN whose payload is in its last bits, of either sign, stays a NaN."""
     codes, scales, _ = quantised(4, 1, 16, 64)

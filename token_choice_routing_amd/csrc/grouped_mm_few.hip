@@ -125,6 +125,11 @@ struct Weights<T, true> {
   __device__ __forceinline__ bf16x8_t step(int i, bool on) const {
     return weights4_bf16(on ? v[i] : 0u, on ? scale : 127u);
   }
+  // The eight weights from column k on (0 unless on), an eighth of them if asked for.
+  __device__ __forceinline__ bf16x8_t one(int k, bool on, bool eighth) const {
+    const uint32_t c = on ? *reinterpret_cast<const uint32_t*>(codes + k / 2) : 0u;
+    return weights4_bf16_divided(c, on ? scales[k / kW4Block] : 127u, eighth);
+  }
 };
 
 template <typename T, bool W4>
@@ -185,8 +190,14 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
         load_rows(s, 0, c);
       };
       Set s0, s1;
+      // lanes (weight row l16) that met a block whose weights may pass the largest float
+      uint64_t top[2] = {0, 0};
       auto multiply = [&](Set& s, int c) __attribute__((always_inline)) {
         if (c >= c1) return;
+        if constexpr (W4) {
+#pragma unroll
+          for (int b = 0; b < 2; ++b) top[b] |= ballot(weights4_top(s.w[b].scale));
+        }
         bf16x8_t wf[4][2];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -227,6 +238,45 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
         load(s0, c + 2);
         multiply(s1, c + 1);
         load(s1, c + 3);
+      }
+      // The wavefront's sums once more, where such a block was met: weights of 2^128 and more were
+      // infinities above, which make NaN of a row's parts that are 0 and infinities of products
+      // that are not. The weight rows that hold one are taken divided by 8, and their sums times 8.
+      // (Apart from the loop above, which keeps its registers: such blocks are hardly ever met.)
+      if constexpr (W4) {
+        if (__builtin_expect((top[0] | top[1]) != 0, 0)) {
+          uint32_t eighths[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const uint64_t at = top[b] | top[b] >> 32;
+            eighths[b] = (uint32_t)(at | at >> 16) & 0xffffu;
+          }
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if (MT > 1 && 16 * m >= rows) break;
+            f32x4_t sum[2] = {};
+#pragma unroll 1
+            for (int t = 4 * c0; t < 4 * c1; ++t) {
+              const int k = col(t >> 2, t & 3);
+              const bool on = k < K;
+              Parts<T> a;
+              a.load(arow[m] + (on ? k : 0));
+              a.keep(on);
+              bf16x8_t p[NP];
+              a.split(p);
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const bf16x8_t w = base[b].one(on ? k : 0, on, eighths[b] >> l16 & 1);
+#pragma unroll
+                for (int q = 0; q < NP; ++q) sum[b] = mfma_few<T, W4>(w, p[NP - 1 - q], sum[b]);
+              }
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) acc[m][b][q] = sum[b][q] * (eighths[b] >> (4 * j + q) & 1 ? 8.0f : 1.0f);
+          }
+        }
       }
       // lane: row l16 of 16, four columns 4 j .. of 16
       auto store = [&](int r, int n, const f32x4_t& v) __attribute__((always_inline)) {

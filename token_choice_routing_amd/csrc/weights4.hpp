@@ -29,4 +29,21 @@ __device__ __forceinline__ bf16x8_t weights4_bf16(uint32_t codes, uint32_t scale
   return v;
 }
 
+// Scale bytes with which the codes of 4 and 6 pass the largest float.
+__device__ __forceinline__ bool weights4_top(uint32_t scale) { return scale - 253u < 2u; }
+
+// The same weights, or an eighth of them: exactly too (multiples of 2^-131), and below 2^127 at
+// every scale byte but 255. The bytes below 4 name no eighth: the weights are divided themselves.
+__device__ __forceinline__ bf16x8_t weights4_bf16_divided(uint32_t codes, uint32_t scale, bool eighth) {
+  const bool low = scale < 4u;
+  u32x4_t w = __builtin_bit_cast(u32x4_t, weights4_bf16(codes, eighth && !low && scale != 255u ? scale - 3u : scale));
+  const float by = eighth && low ? 0.125f : 1.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = __uint_as_float(w[i] << 16) * by, hi = __uint_as_float(w[i] & 0xffff0000u) * by;
+    w[i] = __float_as_uint(lo) >> 16 | (__float_as_uint(hi) & 0xffff0000u);
+  }
+  return __builtin_bit_cast(bf16x8_t, w);
+}
+
 }  // namespace moe
