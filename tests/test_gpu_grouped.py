@@ -465,6 +465,40 @@ def test_gemm4_of_every_scale_byte(groups, each, dtype):
     assert fine[:, 253:255].any() and (err <= tol)[fine].all()
 
 
+@pytest.mark.parametrize("groups,each", SPLITS)
+def test_gemm4_of_the_smallest_float32_rows(groups, each):
+    """Rows down to float32's smallest subnormal, with all of their bits, next to ordinary ones and
+    to elements that are not finite, and every scale byte."""
+    n, k = 256, 160
+    say(f"smallest rows, {groups} groups of {each} rows")
+    rows = groups * each
+    gen = torch.Generator(device="cuda").manual_seed(75)
+    off = torch.arange(0, rows + 1, each, dtype=torch.int32, device="cuda")
+    exponents = (-108, -112, -118, -124, -127, -133, -140, -147, 0)
+    e = torch.tensor([exponents[i % len(exponents)] for i in range(rows)], device="cuda")
+    a = torch.randn((rows, k), generator=gen, device="cuda", dtype=torch.float64) * torch.exp2(e.double())[:, None]
+    a[:, 40:44] = 0.0
+    a[-1] = torch.where(torch.arange(k, device="cuda") % 7 == 0, torch.exp2(e[-2].double() - 120), a[-1])
+    a = a.float()
+    codes, _, _ = quantised(76, groups, n, k)
+    scales = torch.arange(256, dtype=torch.uint8, device="cuda")[None, :, None].expand(groups, n, 5).contiguous()
+    h, hs = codes.cpu().numpy(), scales.cpu().numpy()
+    w = G.values4(np.stack([h & 15, h >> 4], -1).reshape(groups, n, k), hs)
+    top = np.repeat(((hs == 253) | (hs == 254)).any(2), each, 0)
+    y = kept((rows, n), "f32")
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, off, codes, scales, y)
+    ref, mag = G.product(host(a), off.cpu().numpy(), w, rows)
+    check_extreme(y, ref, mag, k, top, "all bits of small rows")
+    # without the largest scale bytes, and with an infinity and a NaN in two of the rows
+    scales, top = scales.clamp(max=252), np.zeros_like(top)
+    w = G.values4(np.stack([h & 15, h >> 4], -1).reshape(groups, n, k), scales.cpu().numpy())
+    a[0, 3], a[1, 77] = float("inf"), float("nan")
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, off, codes, scales, y)
+    ref, mag = G.product(np.nan_to_num(host(a), posinf=0.0), off.cpu().numpy(), w, rows)
+    check_extreme(y[2:], ref[2:], mag[2:], k, top[2:], "small rows next to others that are not finite")
+    assert not np.isfinite(host(y)[0]).any() and np.isnan(host(y)[1]).all()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_gemm4_of_values_past_the_largest_float(dtype):
     """Weights of 2^128 and more: exact where the product is not too large, infinite where it

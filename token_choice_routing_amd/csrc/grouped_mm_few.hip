@@ -18,7 +18,8 @@ constexpr int kChunk = 128;  // elements of the reduction that a wavefront takes
 
 // Eight consecutive elements of a as loaded, and as N bf16 parts whose sum they are: 8
 // significant bits each (1 part for bf16, 2 for half, 3 for float32; cut off, not rounded, so
-// that the largest values stay finite). A value that is not finite is its first part.
+// that the largest values stay finite). A value that is not finite is its first part. Bits below
+// bf16's smallest subnormal, 2^-133, are in no part (a float32 of less than 2^-110 may have some).
 template <typename T>
 struct Parts;
 template <>
@@ -82,6 +83,28 @@ struct Parts<float> {
     o[1] = __builtin_bit_cast(bf16x8_t, b);
     o[2] = __builtin_bit_cast(bf16x8_t, c);
   }
+  // What the parts leave out, times 2^64: 16 bits in two parts.
+  __device__ __forceinline__ void left_out(bf16x8_t (&o)[2]) const {
+    u32x4_t a, b;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float r[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        r[h] = cut_rest(cut_rest(cut_rest(__builtin_canonicalizef(v[j >> 1][2 * (j & 1) + h])))) * 0x1p64f;
+      a[j] = high_halves(r[0], r[1]);
+      b[j] = high_halves(cut_rest(r[0]), cut_rest(r[1]));
+    }
+    o[0] = __builtin_bit_cast(bf16x8_t, a);
+    o[1] = __builtin_bit_cast(bf16x8_t, b);
+  }
+  // m: the smallest magnitude but 0 so far, as bits without the sign less 1 (0 becomes the largest)
+  static constexpr uint32_t kWhole = ((127u - 110u) << 24) - 1u;  // 2^-110: from there on nothing is left out
+  __device__ __forceinline__ void smallest(uint32_t& m) const {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2)
+      m = min(min((__float_as_uint(v[j >> 2][j & 3]) << 1) - 1u, (__float_as_uint(v[j >> 2][(j & 3) + 1]) << 1) - 1u), m);
+  }
 };
 
 // A lane's weights of one chunk: of weight row lane % 16 in the MFMA's layout, four 16 x 32
@@ -142,9 +165,11 @@ __device__ __forceinline__ f32x4_t mfma_few(bf16x8_t w, bf16x8_t a, f32x4_t c) {
 }
 
 // KS wavefronts of the workgroup's four share an item's reduction; 4 / KS items run side by
-// side, of neighbouring columns.
+// side, of neighbouring columns. (Two wavefronts a SIMD named, the compiler keeps sums in no
+// accumulation registers, which with the others would leave one of 64 float32 rows: 64 experts of
+// 32 float32 rows, 2048 x 1536: 185 us without, 166 so.)
 template <typename T, bool W4, bool SWIGLU, int KS, int MT>
-__global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) grouped_mm_few_kernel(GroupedMm g) {
   constexpr int kRows = 16 * MT;
   // of more than 16 rows two sixteens in turn (64 experts of 32 rows: 96 -> 69 us in bf16; float32
   // ones would take too many registers: 131 -> 157)
@@ -164,15 +189,23 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
     const int mt = (sg.len[e] + kRows - 1) / kRows, local = it - sg.prefix[e];
     const int n0 = local / mt * WC + wave / KS * OC, r0 = sg.start[e] + local % mt * kRows;
     const int rows = __builtin_amdgcn_readfirstlane(min(kRows, sg.start[e] + sg.len[e] - r0));
-    Weights<T, W4> base[2];
+    auto weights_at = [&](Weights<T, W4> (&w)[2], int l) __attribute__((always_inline)) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-      base[b].at(g, SWIGLU ? b : 0, (int64_t)e * g.n_out + min(n0 + (SWIGLU ? 0 : 16 * b) + l16, g.n_out - 1));
+      for (int b = 0; b < 2; ++b)
+        w[b].at(g, SWIGLU ? b : 0, (int64_t)e * g.n_out + min(n0 + (SWIGLU ? 0 : 16 * b) + l, g.n_out - 1));
+    };
+    Weights<T, W4> base[2];
+    weights_at(base, l16);
     {
       f32x4_t acc[MT][2];
       const T* arow[MT];
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[m][0] = acc[m][1] = f32x4_t{0, 0, 0, 0};
+      auto row_at = [&](int r) __attribute__((always_inline)) {
+        int64_t row = r0 + min(r, rows - 1);
+        if (g.a_rows) row = min<int64_t>(max<int64_t>(g.a_rows[row], 0), g.a_nrows - 1);
+        return static_cast<const T*>(g.a) + row * g.lda;
+      };
       // the element that a lane's step i of chunk c begins at, in the weights' order
       auto col = [&](int c, int i) { return c * kChunk + (W4 ? 32 * j + 8 * i : 32 * i + 8 * j); };
       struct Set {  // a chunk in registers; two in turn
@@ -192,6 +225,7 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
       Set s0, s1;
       // lanes (weight row l16) that met a block whose weights may pass the largest float
       uint64_t top[2] = {0, 0};
+      uint32_t least = ~0u;  // Parts<float>::smallest() of the lane's rows
       auto multiply = [&](Set& s, int c) __attribute__((always_inline)) {
         if (c >= c1) return;
         if constexpr (W4) {
@@ -211,6 +245,7 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             s.a[m % NA][i].keep(col(c, i) < K);
+            if constexpr (W4 && sizeof(T) == 4) s.a[m % NA][i].smallest(least);
             bf16x8_t p[NP];
             if constexpr (W4) s.a[m % NA][i].split(p);
             else p[0] = __builtin_bit_cast(bf16x8_t, s.a[m % NA][i].v);
@@ -226,11 +261,7 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
       for (int b = 0; b < 2; ++b)
         if (c0 < c1) s0.w[b].load(base[b], c0, j, K);
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        int64_t row = r0 + min(16 * m + l16, rows - 1);
-        if (g.a_rows) row = min<int64_t>(max<int64_t>(g.a_rows[row], 0), g.a_nrows - 1);
-        arow[m] = static_cast<const T*>(g.a) + row * g.lda;
-      }
+      for (int m = 0; m < MT; ++m) arow[m] = row_at(16 * m + l16);
       if (c0 < c1) load_rows(s0, 0, c0);
       load(s1, c0 + 1);
       for (int c = c0; c < c1; c += 2) {
@@ -239,12 +270,19 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
         multiply(s1, c + 1);
         load(s1, c + 3);
       }
-      // The wavefront's sums once more, where such a block was met: weights of 2^128 and more were
-      // infinities above, which make NaN of a row's parts that are 0 and infinities of products
-      // that are not. The weight rows that hold one are taken divided by 8, and their sums times 8.
-      // (Apart from the loop above, which keeps its registers: such blocks are hardly ever met.)
+      // The wavefront's sums once more, where such a block was met or a row has bits too small for
+      // bf16. Weights of 2^128 and more were infinities above, which make NaN of a row's parts that
+      // are 0 and infinities of products that are not: the weight rows that hold one are taken
+      // divided by 8, and their sums times 8. The bits left out above have sums of their own, times
+      // 2^64. (Apart from the loop above, which keeps its registers, the pointers' too: both are
+      // hardly ever met.)
       if constexpr (W4) {
-        if (__builtin_expect((top[0] | top[1]) != 0, 0)) {
+        bool small_rows = false;
+        if constexpr (sizeof(T) == 4) small_rows = ballot(least < Parts<T>::kWhole) != 0;
+        if (__builtin_expect((top[0] | top[1]) != 0 || small_rows, 0)) {
+          const int l16 = opaque_v((int)threadIdx.x) & 15;
+          Weights<T, W4> base[2];
+          weights_at(base, l16);
           uint32_t eighths[2];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
@@ -254,27 +292,34 @@ __global__ void __launch_bounds__(256) grouped_mm_few_kernel(GroupedMm g) {
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
             if (MT > 1 && 16 * m >= rows) break;
-            f32x4_t sum[2] = {};
+            const T* const row = row_at(16 * m + l16);
+            f32x4_t sum[2] = {}, small[2] = {};
 #pragma unroll 1
             for (int t = 4 * c0; t < 4 * c1; ++t) {
               const int k = col(t >> 2, t & 3);
               const bool on = k < K;
               Parts<T> a;
-              a.load(arow[m] + (on ? k : 0));
+              a.load(row + (on ? k : 0));
               a.keep(on);
-              bf16x8_t p[NP];
+              bf16x8_t p[NP], r[2];
               a.split(p);
+              if constexpr (sizeof(T) == 4) a.left_out(r);
 #pragma unroll
               for (int b = 0; b < 2; ++b) {
                 const bf16x8_t w = base[b].one(on ? k : 0, on, eighths[b] >> l16 & 1);
 #pragma unroll
                 for (int q = 0; q < NP; ++q) sum[b] = mfma_few<T, W4>(w, p[NP - 1 - q], sum[b]);
+                if constexpr (sizeof(T) == 4) {
+                  small[b] = mfma_few<T, W4>(w, r[1], small[b]);
+                  small[b] = mfma_few<T, W4>(w, r[0], small[b]);
+                }
               }
             }
 #pragma unroll
             for (int b = 0; b < 2; ++b)
 #pragma unroll
-              for (int q = 0; q < 4; ++q) acc[m][b][q] = sum[b][q] * (eighths[b] >> (4 * j + q) & 1 ? 8.0f : 1.0f);
+              for (int q = 0; q < 4; ++q)
+                acc[m][b][q] = (sum[b][q] + small[b][q] * 0x1p-64f) * (eighths[b] >> (4 * j + q) & 1 ? 8.0f : 1.0f);
           }
         }
       }
