@@ -534,10 +534,10 @@ def test_gemm4_of_a_nan_with_any_payload():
 
 
 # Kernel forms that the sizes above leave out, with 256 CUs.
-# At most 16 rows an expert and at least 1024 items: a wavefront takes the whole reduction (of 16
-# rows). 968 columns end inside a panel of 128 (64 for gate/up): of its four wavefronts one has
+# At most 16 rows an expert, of the 16-bit product 256 in all, and at least 1024 items: a wavefront
+# takes the whole reduction (of 16 rows). 968 columns end inside a panel of 128 (64 for gate/up): of its four wavefronts one has
 # columns in part and one or more have none.
-FEW_WHOLE = [0, 3, 9, 1, 5, 0, 2, 8, 4, 7, 16, 0] * 5
+FEW_WHOLE = [0, 3, 9, 1, 5, 0, 2, 8, 4, 2, 16, 0] * 5
 # More than 16 rows an expert: 64 rows an item, a wavefront with the whole reduction.
 TALL_WHOLE = [17, 70, 0, 33, 64, 65, 1, 48, 20, 5, 16, 130]
 
@@ -549,12 +549,30 @@ TALL_WHOLE = [17, 70, 0, 33, 64, 65, 1, 48, 20, 5, 16, 130]
 def test_few_rows_with_the_whole_reduction(n, k, gather, out, dtype):
     say(f"few rows, whole reduction n {n} k {k} {dtype} -> {out} gather {gather}")
     rows, off, a_rows, a, _, w = make(51, FEW_WHOLE, n, k, dtype, T=40 if gather else None, first=1)
-    assert rows <= 16 * len(FEW_WHOLE) and (rows // 16 + len(FEW_WHOLE)) * (n // 32) >= 1024
+    assert rows <= 256 and (rows // 16 + len(FEW_WHOLE)) * (n // 32) >= 1024
     y = kept((rows, n + 8), out)
     tcr.moe_grouped_mm(a, off, w, y[:, :n], a_rows=a_rows)
     ha, hf, hw, hr = arrays(a, off, w, a_rows)
     check(y[:, :n], *G.product(ha, hf, hw, rows, hr), k, out, "out")
     assert bool((y[:, n:] == KEEP).all())
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("groups", [7, 16, 64, 80])
+def test_on_both_sides_of_few_rows(groups, dtype):
+    """The most rows that count as few (4 an expert on average, or 256 of at most 16) and one row
+    more, evenly and all of one expert."""
+    n, k = 136, 200
+    most = min(16 * groups, max(4 * groups, 256))
+    for total in (most, most + 1):
+        even = [total // groups + (e < total % groups) for e in range(groups)]
+        for counts in (even, [0] * (groups - 1) + [total]):
+            say(f"{total} rows of {groups} experts, {max(counts)} of one, {dtype}")
+            rows, off, a_rows, a, _, w = make(53, counts, n, k, dtype, behind=0, T=90)
+            y = kept((rows, n), dtype)
+            tcr.moe_grouped_mm(a, off, w, y, a_rows=a_rows)
+            ha, hf, hw, hr = arrays(a, off, w, a_rows)
+            check(y, *G.product(ha, hf, hw, rows, hr), k, dtype, "out")
 
 
 @pytest.mark.parametrize("dtype", TYPES)

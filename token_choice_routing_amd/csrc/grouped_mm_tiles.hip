@@ -551,9 +551,16 @@ hipError_t launch_for(const GroupedMm& g, int num_cus, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_grouped_mm(const GroupedMm& g, int num_cus, hipStream_t s) {
-  // few rows: 73 us against 80 with 4 rows of each of 64 experts (n 2048, k 1536), 81 and 84
-  // with 16, 111 and 87 with 32; 2 rows of two experts 8 and 18
-  const bool few = g.form == kMm && g.dtype != MOE_F32 && g.rows <= 16 * (int64_t)g.groups;
+  // Few rows. us there and in the tiles, 2048 x 1536, bf16:
+  //   2 rows of 8 experts 8 and 16, 12 of each of 8: 14 and 17 (768 x 1024, 16 of each of 16: 11 and 14)
+  //   64 experts, 1, 4, 8 or 16 rows each: 75 and 80, 76 and 82, 79 and 85, 85 and 87
+  //   as many rows by Zipf's law: 39 and 42, 71 and 79, 99 and 89, 118 and 105; all of one expert: 22
+  //   and 19, 23 and 21, 39 and 21, 70 and 24 (128 experts, 16 on average: 133 and 28)
+  // The weights of an expert are read again for every 16 of its rows there, and only the device
+  // knows which expert has how many. So: up to 4 rows an expert on average, which keeps what even
+  // rows gain and bounds what one large expert costs, or up to 256 rows of 16 on average.
+  const bool few = g.form == kMm && g.dtype != MOE_F32 && g.rows <= 16 * (int64_t)g.groups &&
+                   g.rows <= std::max<int64_t>(4 * (int64_t)g.groups, 256);
   if (few || g.form == kMm4 || g.form == kMm4Swiglu) return launch_grouped_mm_few(g, num_cus, s);
   return with_rows(g.dtype, [&](auto* t) { return launch_for<std::remove_pointer_t<decltype(t)>>(g, num_cus, s); });
 }
