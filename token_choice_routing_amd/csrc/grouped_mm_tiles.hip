@@ -247,9 +247,12 @@ grouped_mm_tiles_kernel(GroupedMm g) {
       const int k = k0 + (KJ ? krow(piece, BN) : lc * EC);
       uint32_t off = joff[p];
       if constexpr (ROWS) {
+        // (of four the compiler would otherwise make an array in scratch memory, indexed by lane: a
+        // load and a wait for every tile in flight)
         int row = idx[p][0];
 #pragma unroll
-        for (int q = 1; q < KPP; ++q) row = lane / (BN * ES / 16) >= q ? idx[p][q] : row;
+        for (int q = 1; q < KPP; ++q)
+          row = lane / (BN * ES / 16) >= q ? (KPP > 2 ? opaque_v(idx[p][q]) : idx[p][q]) : row;
         off = off == kPast ? kPast : off + (uint32_t)min(max(row, 0), last_row) * lda_bytes;
       }
       buffer_load_lds16(rj, whole || k < lklen ? off : kPast,
