@@ -437,7 +437,9 @@ moe_status moe_grouped_mm_wgrad(int32_t dtype, int32_t n_groups, int32_t n_out, 
  * a NaN or an infinity has scale byte 255 and codes 0 and stands for NaN.
  * |w - value| <= 2^e / 4 up to 2 steps of 2^e, 2^e / 2 up to 4, 2^e up to 6, and below 2^(e+1)
  * beyond (amax lies in [4, 8) steps, so always below amax / 4; blocks below 2^-124 apart).
- * rows >= 0 (0 is a no-op), rows * cols below 2^40. No workspace.
+ * rows >= 0 (0 is a no-op), rows * cols below 2^40. No workspace. Scale bytes may begin at any
+ * multiple of 8, here and in moe_grouped_gemm4, so that experts of n_out * cols weights can be
+ * packed one by one into their places (n_out a multiple of 8).
  */
 moe_status moe_weights4_pack(int64_t rows, int32_t cols, int32_t dtype, const void* w, uint8_t* codes, uint8_t* scales,
                              moe_stream stream);

@@ -399,6 +399,33 @@ def test_gemm4_scales_and_values_at_the_ends(dtype):
     assert (np.abs(got - ref) <= tol)[fine].all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+def test_experts_packed_and_used_one_by_one(dtype):
+    """Each expert's codes and scale bytes in their places, which begin at odd multiples of 8 for
+    the scale bytes, equal those of all experts at once; and so do products with the last ones."""
+    groups, n, k, rows = 5, 40, 96, 21
+    say(f"experts one by one, {dtype}")
+    gen = torch.Generator(device="cuda").manual_seed(41)
+    w = torch.randn((groups, n, k), generator=gen, device="cuda").to(TYPES[dtype])
+    cs, ss = tcr.weights4_shapes(w.shape)
+    sets = [(torch.full(cs, 99, dtype=torch.uint8, device="cuda"), torch.full(ss, 99, dtype=torch.uint8, device="cuda"),
+             kept(w.shape, dtype)) for _ in range(2)]
+    (c, s, v), (c1, s1, v1) = sets
+    tcr.moe_weights4_pack(w, c, s)
+    tcr.moe_weights4_unpack(c, s, v)
+    for e in range(groups):
+        assert s1[e].data_ptr() % 16 == (8 if e % 2 else 0)
+        tcr.moe_weights4_pack(w[e], c1[e], s1[e])
+        tcr.moe_weights4_unpack(c1[e], s1[e], v1[e])
+    assert bool((c == c1).all()) and bool((s == s1).all()) and bool((v == v1).all())
+    a = torch.randn((rows, k), generator=gen, device="cuda").to(TYPES[dtype])
+    off = torch.tensor([0, 9, 9, 20, 20, 21], dtype=torch.int32, device="cuda")
+    full, part = kept((rows, n), dtype), kept((rows, n), dtype)
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_GATE_UP, a, off, c, s, full, c, s)
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_GATE_UP, a, off[1:].clone(), c1[1:], s1[1:], part, c1[1:], s1[1:])
+    assert bool((part[:9] == KEEP).all()) and bool((part[9:] == full[9:]).all())
+
+
 # groups, rows of each and the wavefronts that share a reduction (n 256): four or one, of 16 or
 # of 64 rows
 SPLITS = [(1, 5), (1, 40), (128, 2), (120, 17)]

@@ -139,6 +139,16 @@ def test_weights4_sizes_whose_product_passes_64_bits(lib):
         assert lib.moe_weights4_pack(rows, cols, MOE_F32, MIS, FAKE, FAKE, None) == MOE_ERR_ALIGN, (rows, cols)
 
 
+def test_scale_bytes_at_multiples_of_8(lib):
+    """Where one expert's scale bytes begin among those of all."""
+    for s, status in ((FAKE + 8, MOE_OK), (FAKE + 24, MOE_OK), (FAKE + 2, MOE_ERR_ALIGN), (FAKE + 12, MOE_ERR_ALIGN)):
+        assert lib.moe_weights4_pack(0, 64, MOE_F16, FAKE, FAKE, s, None) == status
+        assert lib.moe_weights4_unpack(0, 64, MOE_F16, FAKE, s, FAKE, None) == status
+        assert _gemm4(lib, s0=s, rows=0) == status
+        assert _gemm4(lib, s1=s, rows=0) == status
+    assert lib.moe_weights4_pack(0, 64, MOE_F16, FAKE, FAKE + 8, FAKE, None) == MOE_ERR_ALIGN
+
+
 def test_binding_refuses():
     """Tensors on the host, of another type or shape, or missing."""
     z = torch.zeros

@@ -795,6 +795,13 @@ static moe_status check_mm_a(const void* a, int64_t lda, int32_t k_dim, const in
   return maybe(a_rows);
 }
 
+// Scale bytes of 4-bit weights, which the kernels read one by one: those of an expert (n_out a
+// multiple of 8) begin at a multiple of 8 among the others'.
+static moe_status need_scales(const uint8_t* p) {
+  if (!p) return MOE_ERR_ARG;
+  return reinterpret_cast<uintptr_t>(p) & 7u ? MOE_ERR_ALIGN : MOE_OK;
+}
+
 moe_status moe_grouped_mm(int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows, const void* a,
                           int64_t lda, const int32_t* a_rows, int64_t a_nrows, const int32_t* offsets, const void* w,
                           int32_t out_dtype, void* out, int64_t ldo, moe_stream stream) {
@@ -893,10 +900,10 @@ moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_
   if (k_dim % 32) return MOE_ERR_ARG;
   MOE_TRY(check_mm_a(a, lda, k_dim, a_rows, a_nrows, dtype, rows));
   MOE_TRY(need(codes0));
-  MOE_TRY(need(scales0));
+  MOE_TRY(need_scales(scales0));
   if (op == MOE_GEMM_GATE_UP) {
     MOE_TRY(need(codes1));
-    MOE_TRY(need(scales1));
+    MOE_TRY(need_scales(scales1));
   }
   MOE_TRY(check_mm_rows(out, ldo, n_out));
   if (rows == 0) return MOE_OK;
@@ -935,7 +942,7 @@ moe_status moe_weights4_pack(int64_t rows, int32_t cols, int32_t dtype, const vo
   MOE_TRY(check_weights4(rows, cols, dtype));
   MOE_TRY(need(w));
   MOE_TRY(need(codes));
-  MOE_TRY(need(scales));
+  MOE_TRY(need_scales(scales));
   if (rows == 0) return MOE_OK;
   MOE_TRY(no_pending_error());
   HIP_TRY(launch_weights4_pack(dtype, w, rows * (cols / 32), codes, scales, static_cast<hipStream_t>(stream)));
@@ -946,7 +953,7 @@ moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const 
                                void* out, moe_stream stream) {
   MOE_TRY(check_weights4(rows, cols, dtype));
   MOE_TRY(need(codes));
-  MOE_TRY(need(scales));
+  MOE_TRY(need_scales(scales));
   MOE_TRY(need(out));
   if (rows == 0) return MOE_OK;
   MOE_TRY(no_pending_error());
