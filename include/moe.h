@@ -456,10 +456,13 @@ moe_status moe_weights4_unpack(int64_t rows, int32_t cols, int32_t dtype, const 
  * [n_groups][n_out][k_dim / 32] stand for; a, a_rows, offsets, out, the types and the limits
  * are those of moe_grouped_mm (pieces of 16 x 16 instead of 32 x 32), k_dim a multiple of 32.
  * Products of the weights with a are exact (of weights of 2^128 and more too: an output is
- * infinite only if its sum or a part of it is too large), sums in float32. Any number of rows is taken, but
- * an expert's weights are read and converted again for every 16 of its rows (64 where rows >
- * 16 n_groups): from about 32 rows an expert, moe_weights4_unpack once and moe_grouped_mm take
- * less time. No workspace.
+ * infinite only if its sum or a part of it is too large), sums in float32. Any number of rows is
+ * taken, but an expert's weights are read and converted again for every 16 of its rows (64 where
+ * rows > 16 n_groups). 64 experts of 2048 x 1536, bf16: 32 rows an expert take 72 us
+ * (moe_grouped_mm of unpacked weights 94, unpacking them 95), 64 rows 114 (101), 128 rows 215
+ * (111): from about 64 rows on weights that stay unpacked, from about 96 also unpacking them for
+ * the call, take less time. silu(z) is -0 below z = -88.7, where exp(-z) is no float32. No
+ * workspace.
  */
 moe_status moe_grouped_gemm4(int32_t op, int32_t dtype, int32_t n_groups, int32_t n_out, int32_t k_dim, int64_t rows,
                              const void* a, int64_t lda, const int32_t* a_rows, int64_t a_nrows,

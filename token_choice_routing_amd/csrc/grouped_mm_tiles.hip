@@ -12,11 +12,13 @@
 // fit the registers of two wavefronts a SIMD (208 of 256), and four stages the LDS (128 KB). A
 // wavefront reads half a stage's fragments while it multiplies the other half, with one barrier
 // a stage; the loads run four stages ahead and on into the next tiles. 8192^3 bf16: 860-920 us
-// (1.20-1.28 PF; the library's product 1.19). 32970 rows of 64 experts, 1536 x 2048: product 250
-// us, data gradient 247, weight gradient (float32) 265. What bounds them there: the matrix pipe
-// is busy 40-44% of the time; weights that come from memory once (225 us with equal experts of
-// 512 rows, 190 with one expert), partly filled row tiles and the last round of tiles; in the
-// weight gradient the 805 MB of stores (182 us without them).
+// (1.20-1.28 PF; the library's product of this layout 670-711, of row-major B 790-875). 32889 rows of 64 experts, 22 to 2794 each, 1536 x
+// 2048: product 256 us, 262 of gathered rows; data gradient 236; weight gradient (float32) 303, 324
+// of gathered rows, 577 added to an earlier one (460 to 558 rows each: 250 and 257, 236, 296 and
+// 308, 521). What bounds them there: the matrix pipe is busy 40-44% of the time; weights that come
+// from memory once (product 229 us with equal experts of 512 rows, 201 with one expert), partly
+// filled row tiles and the last round of tiles; in the weight gradient the 805 MB of stores (182
+// us without them), and with an addend a load, a wait and a store for every 16 bytes of a lane.
 #include <algorithm>
 
 #include "grouped_mm.hpp"

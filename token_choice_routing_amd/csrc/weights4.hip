@@ -11,7 +11,8 @@ namespace {
 
 // Both directions move bytes: 4.25 bits a weight on one side, 16 or 32 on the other. Four lanes
 // share a block, eight weights each, so a wavefront's loads and stores are contiguous. 64 x
-// 1536 x 2048 bf16: packed in 86 us, unpacked in 91 (5.9 and 5.6 TB/s; a large copy 5.1 to 5.4).
+// 1536 x 2048 bf16: packed in 88 us, unpacked in 94 (5.8 and 5.4 TB/s; a large copy 5.1 to 5.4); in
+// turn, each on what the other has just written, 104 and 82 (there and back 186).
 // One lane a block and the rounding in float arithmetic took 258 us there and back, four lanes
 // with that rounding 134 us there.
 
