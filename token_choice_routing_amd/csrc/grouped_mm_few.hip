@@ -165,9 +165,9 @@ __device__ __forceinline__ f32x4_t mfma_few(bf16x8_t w, bf16x8_t a, f32x4_t c) {
 }
 
 // KS wavefronts of the workgroup's four share an item's reduction; 4 / KS items run side by
-// side, of neighbouring columns. (Two wavefronts a SIMD named, the compiler keeps sums in no
-// accumulation registers, which with the others would leave one of 64 float32 rows: 64 experts of
-// 32 float32 rows, 2048 x 1536: 185 us without, 166 so.)
+// side, of neighbouring columns. (Two wavefronts a SIMD are named for the items of 64 float32 rows:
+// the compiler then puts no sums into accumulation registers, with which it ends at one. 64
+// experts of 32 gathered float32 rows, 2048 x 1536: 211 us without, 166 so.)
 template <typename T, bool W4, bool SWIGLU, int KS, int MT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) grouped_mm_few_kernel(GroupedMm g) {
   constexpr int kRows = 16 * MT;
