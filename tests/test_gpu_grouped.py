@@ -526,6 +526,26 @@ def test_gemm4_of_the_smallest_float32_rows(groups, each):
     assert not np.isfinite(host(y)[0]).any() and np.isnan(host(y)[1]).all()
 
 
+@pytest.mark.parametrize("groups,each", SPLITS)
+def test_gemm4_rows_next_to_the_smallest_keep_their_bits(groups, each):
+    """A row's outputs do not depend on whether a row or a weight row beside it is extreme."""
+    n, k = 256, 160
+    say(f"bits next to extremes, {groups} groups of {each} rows")
+    rows = groups * each
+    gen = torch.Generator(device="cuda").manual_seed(77)
+    off = torch.arange(0, rows + 1, each, dtype=torch.int32, device="cuda")
+    a = torch.randn((rows, k), generator=gen, device="cuda")
+    codes, scales, _ = quantised(78, groups, n, k)
+    first, second = kept((rows, n), "f32"), kept((rows, n), "f32")
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, off, codes, scales, first)
+    a[::each, 17] = 1e-37
+    scales[:, 9::16, 2] = 254
+    tcr.moe_grouped_gemm4(tcr.MOE_GEMM_DOWN, a, off, codes, scales, second)
+    same = torch.ones((rows, n), dtype=torch.bool, device="cuda")
+    same[::each], same[:, 9::16] = False, False
+    assert bool((first == second)[same].all()) and not bool((first == second)[~same].all())
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_gemm4_of_values_past_the_largest_float(dtype):
     """Weights of 2^128 and more: exact where the product is not too large, infinite where it
